@@ -14,10 +14,15 @@ from .ops import (  # noqa: F401
     centroid_compensated_attention,
     device_status,
     error_aware_block_mask,
+    paged_block_tables,
+    paged_chunk_attention,
+    paged_qk_norm_append,
     per_kv_head_attention,
     probe_dense_attention,
     probe_budget_block_mask,
     probe_residual_correction,
+    qk_norm_rotation,
+    qk_norm_rotation_backward,
     response_coupled_partition,
     select_probe_rows,
     sliding_tile_block_mask,

@@ -15,6 +15,7 @@ BSA_ERR_TIMEOUT = -4
 BSA_ERR_WORKSPACE = -5
 BSA_BF16 = 0
 BSA_F32 = 1
+BSA_F16 = 2
 
 
 class BsaError(RuntimeError):
@@ -29,6 +30,18 @@ class Shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int),
                 ("Sq", ctypes.c_int), ("Sk", ctypes.c_int), ("D", ctypes.c_int),
                 ("dtype", ctypes.c_int)]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64), ("stride_s", ctypes.c_int64)]
+
+
+class PagedCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int),
+                ("page", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+                ("dtype", ctypes.c_int)] + \
+               [(f"{x}_{y}_stride", ctypes.c_int64) for x in "kv" for y in ("page", "head", "row")]
 
 
 _vp, _i, _f, _sz, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_int64
@@ -79,6 +92,21 @@ SIGNATURES = {
     "bsa_mask_cache_layer_gate": (_i, [_vp, _vp, _i, _i, _f, _f, _vp]),
     "bsa_mask_cache_update": (_i, [_vp, _vp, _vp, _vp, _vp]),
     "bsa_mask_cache_reset": (_i, [_vp, _vp]),
+    "bsa_qk_norm_rotation": (
+        _i, [Heads, Heads, Shape, _vp, _vp, _i, _vp, _vp, _i, _vp, _i64, _f, _i, Heads, Heads, _vp]),
+    "bsa_qk_norm_rotation_workspace_bytes": (_sz, [Shape]),
+    "bsa_qk_norm_rotation_backward": (
+        _i, [Heads, Heads, Heads, Heads, Shape, _vp, _vp, _i, _vp, _vp, _i, _vp, _i64, _f, _i,
+             Heads, Heads, _vp, _vp, _vp, _sz, _vp]),
+    "bsa_paged_block_tables": (
+        _i, [_vp, _vp, _i, _vp, _i, _i64, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]),
+    "bsa_paged_qk_norm_append": (
+        _i, [Heads, Heads, Heads, _i, _i, _vp, _vp, _i, _vp, _vp, _i, _vp, _vp, _f, _i, Heads,
+             PagedCache, _vp]),
+    "bsa_paged_attention_workspace_bytes": (_sz, [PagedCache, _i, _i, _i, _i, _i]),
+    "bsa_paged_chunk_attention": (
+        _i, [Heads, PagedCache, _vp, _i, _i64, _vp, _vp, _i, _i, _i, _i, _vp, _i64, _i64, _f, _i,
+             Heads, _vp, _sz, _vp]),
 }
 
 _lib = None

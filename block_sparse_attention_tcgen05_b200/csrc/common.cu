@@ -114,6 +114,24 @@ int make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, 
   return BSA_OK;
 }
 
+int make_tmap_4d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, int elem_bytes,
+                 const uint64_t (&d)[4], const uint64_t (&st)[3], const uint32_t (&bx)[4]) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(BSA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  if (reinterpret_cast<uintptr_t>(base) % 16 || st[0] % 16 || st[1] % 16 || st[2] % 16 ||
+      (bx[0] * elem_bytes) % 16)
+    return fail(BSA_ERR_INVALID_ARG, "tensor map operands not 16-byte aligned");
+  cuuint64_t dims[4] = {d[0], d[1], d[2], d[3]};
+  cuuint64_t strides[3] = {st[0], st[1], st[2]};
+  cuuint32_t box[4] = {bx[0], bx[1], bx[2], bx[3]};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, dtype, 4, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(BSA_ERR_CUDA, "cuTensorMapEncodeTiled (4d) failed: %d", int(r));
+  return BSA_OK;
+}
+
 // Label of every token of a T x H x W grid for tiles (tt, th, tw), edge tiles partial.
 __global__ void tile_labels_kernel(int T, int H, int W, int tt, int th, int tw, int nH, int nW,
                                    int32_t* __restrict__ labels) {

@@ -45,6 +45,14 @@ int make_tmap_3d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, 
                  uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1_bytes,
                  uint64_t stride2_bytes, uint32_t box0, uint32_t box1, uint32_t box2);
 
+// Same, 4-D: dims (inner .. outer) with byte strides of the outer three.
+int make_tmap_4d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, int elem_bytes,
+                 const uint64_t (&dims)[4], const uint64_t (&stride_bytes)[3],
+                 const uint32_t (&box)[4]);
+
+// Argument checks of a paged cache: type, page size, strides, alignment.
+int check_paged_cache(const bsa_paged_cache& c);
+
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 // Kernel timing hooks (bsa_profile_*): when enabled, the launch sites of the main

@@ -1,0 +1,676 @@
+// Per-head RMS norms of queries and keys with the position rotation in the same pass, its
+// backward pass, and the same pass with the keys and values scattered into a paged cache.
+//
+// A row of D values is held by D/8 lanes, eight values each, so a warp holds 2 (D = 128) or
+// 4 (D = 64) rows and the sum of squares is a butterfly over 16 or 8 lanes. The lane's eight
+// values are the four pairs 4l .. 4l+3 of the rotation in both conventions: eight neighbours
+// (pairs of neighbours), or four values of each half (pairs half a row apart), so no value
+// moves between lanes and each lane reads four cosines and four sines. A lane group keeps
+// its token and walks over heads, kUnroll rows at a time: the cosines, sines and both
+// weights are read once per token and group.
+//
+// Everything is fp32 between the load and the one rounding of the store. The pass is bound
+// by HBM: each input row is read once, each output row written once.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace bsa {
+
+namespace {
+
+constexpr int kNormThreads = 256;
+
+template <typename T>
+struct Vec8;  // eight values of a lane: 16 bytes of a 16-bit type, 32 of fp32
+
+__device__ __forceinline__ uint4 ld16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ uint2 ld8(const void* p) { return *reinterpret_cast<const uint2*>(p); }
+
+template <typename T>
+__device__ __forceinline__ void unpack2(uint32_t u, float& a, float& b) {
+  if constexpr (sizeof(T) == 2) {
+    if constexpr (std::is_same<T, __half>::value) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
+      a = f.x;
+      b = f.y;
+    } else {
+      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
+      a = f.x;
+      b = f.y;
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (std::is_same<T, __half>::value) {
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+  } else {
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+}
+
+// The raw bits of a lane's eight values (kept unconverted while several rows are in flight).
+template <typename T>
+struct Raw {
+  uint32_t w[2 * sizeof(T)];
+};
+
+// Lane l of a row: values 8l .. 8l+7 (interleaved pairs) or 4l .. 4l+3 and D/2 + 4l ..
+template <typename T, int D, bool INTER>
+__device__ __forceinline__ Raw<T> load_row(const T* row, int l) {
+  Raw<T> r;
+  if constexpr (INTER) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
+      const uint4 u = ld16(row + 8 * l + 4 * i);
+      r.w[4 * i] = u.x;
+      r.w[4 * i + 1] = u.y;
+      r.w[4 * i + 2] = u.z;
+      r.w[4 * i + 3] = u.w;
+    }
+  } else if constexpr (sizeof(T) == 2) {
+    const uint2 a = ld8(row + 4 * l), b = ld8(row + D / 2 + 4 * l);
+    r.w[0] = a.x;
+    r.w[1] = a.y;
+    r.w[2] = b.x;
+    r.w[3] = b.y;
+  } else {
+    const uint4 a = ld16(row + 4 * l), b = ld16(row + D / 2 + 4 * l);
+    r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+    r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w;
+  }
+  return r;
+}
+
+// Raw bits to pairs: a[i], b[i] are the two members of pair 4l + i.
+template <typename T, bool INTER>
+__device__ __forceinline__ void to_pairs(const Raw<T>& r, float (&a)[4], float (&b)[4]) {
+  float f[8];
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack2<T>(r.w[i], f[2 * i], f[2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r.w[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[i] = INTER ? f[2 * i] : f[i];
+    b[i] = INTER ? f[2 * i + 1] : f[4 + i];
+  }
+}
+
+template <typename T, int D, bool INTER>
+__device__ __forceinline__ void store_row(T* row, int l, const float (&a)[4], const float (&b)[4]) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[INTER ? 2 * i : i] = a[i];
+    f[INTER ? 2 * i + 1 : 4 + i] = b[i];
+  }
+  if constexpr (sizeof(T) == 2) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pack2<T>(f[2 * i], f[2 * i + 1]);
+    if constexpr (INTER) {
+      *reinterpret_cast<uint4*>(row + 8 * l) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      *reinterpret_cast<uint2*>(row + 4 * l) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(row + D / 2 + 4 * l) = make_uint2(w[2], w[3]);
+    }
+  } else {
+    T* p = INTER ? row + 8 * l : row + 4 * l;
+    T* q = INTER ? row + 8 * l + 4 : row + D / 2 + 4 * l;
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4*>(q) = make_float4(f[4], f[5], f[6], f[7]);
+  }
+}
+
+template <typename T, int D, bool INTER>
+__device__ __forceinline__ void load_weight(const void* w, int f32, int l, float (&a)[4],
+                                            float (&b)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int da = INTER ? 8 * l + 2 * i : 4 * l + i;
+    const int db = INTER ? da + 1 : D / 2 + 4 * l + i;
+    if (f32) {
+      a[i] = static_cast<const float*>(w)[da];
+      b[i] = static_cast<const float*>(w)[db];
+    } else {
+      a[i] = static_cast<float>(static_cast<const T*>(w)[da]);
+      b[i] = static_cast<float>(static_cast<const T*>(w)[db]);
+    }
+  }
+}
+
+// Sum over the D/8 lanes of a row (every lane gets it).
+template <int D>
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+  for (int o = D / 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+struct HeadsIn {
+  const void* p;
+  int64_t sb, sh, ss;
+};
+struct HeadsOut {
+  void* p;
+  int64_t sb, sh, ss;
+};
+
+struct NormArgs {
+  HeadsIn q, k, v;
+  HeadsOut qo, ko;
+  int B, S, Hq, Hkv;
+  int heads;      // rows of a token: Hq + Hkv (+ Hkv values for the paged form)
+  int per_group;  // heads that one lane group walks over
+  const void *qw, *kw;
+  int w_f32;
+  const float *cos, *sin;
+  int n_pos;
+  const int32_t* positions;
+  int64_t pos_b;
+  float eps;
+  // paged destination of keys and values
+  const int32_t* slots;
+  void *kc, *vc;
+  int64_t kp, kh, kr, vp, vh, vr;
+  int page_shift, n_slots;
+};
+
+// -1 = skip silently, -2 = skip and report
+__device__ __forceinline__ int checked_position(const int32_t* positions, int64_t pos_b, int b,
+                                                int s, int n_pos) {
+  const int p = positions ? positions[b * pos_b + s] : s;
+  if (p >= 0 && p < n_pos) return p;
+  return p == -1 ? -1 : -2;
+}
+
+constexpr int kNormSite = 120;
+
+// One lane group per (token, run of per_group heads); grid (token groups, head runs).
+template <typename T, int D, bool INTER, bool PAGED>
+__global__ void __launch_bounds__(kNormThreads) norm_rotation_kernel(const NormArgs a) {
+  constexpr int L = D / 8;
+  constexpr int kUnroll = sizeof(T) == 2 ? 4 : 2;
+  const int l = threadIdx.x % L;
+  const int64_t tok = static_cast<int64_t>(blockIdx.x) * (kNormThreads / L) + threadIdx.x / L;
+  const int64_t ntok = static_cast<int64_t>(a.B) * a.S;
+  const bool in = tok < ntok;
+  const int b = in ? static_cast<int>(tok / a.S) : 0, s = in ? static_cast<int>(tok % a.S) : 0;
+  int pos = in ? checked_position(a.positions, a.pos_b, b, s, a.n_pos) : -1;
+  if (pos == -2 && l == 0) report_device_error(kStatusBadLabel, kNormSite);
+  const bool live = pos >= 0;
+  if (pos < 0) pos = 0;
+  int64_t kdst = 0, vdst = 0;
+  bool put = false;
+  if constexpr (PAGED) {
+    const int slot = live ? a.slots[s] : -1;
+    put = slot >= 0 && slot < a.n_slots;
+    if (live && !put && slot != -1 && l == 0) report_device_error(kStatusBadLabel, kNormSite + 1);
+    if (put) {
+      const int64_t page = slot >> a.page_shift, row = slot & ((1 << a.page_shift) - 1);
+      kdst = page * a.kp + row * a.kr;
+      vdst = page * a.vp + row * a.vr;
+    }
+  }
+  float c[4] = {}, sn[4] = {};
+  if (live) {
+    const float4 c4 = *reinterpret_cast<const float4*>(a.cos + static_cast<int64_t>(pos) * (D / 2) + 4 * l);
+    const float4 s4 = *reinterpret_cast<const float4*>(a.sin + static_cast<int64_t>(pos) * (D / 2) + 4 * l);
+    c[0] = c4.x; c[1] = c4.y; c[2] = c4.z; c[3] = c4.w;
+    sn[0] = s4.x; sn[1] = s4.y; sn[2] = s4.z; sn[3] = s4.w;
+  }
+  const int h_begin = blockIdx.y * a.per_group;
+  const int h_end = min(a.heads, h_begin + a.per_group);
+  const T* qrow = static_cast<const T*>(a.q.p) + b * a.q.sb + s * a.q.ss;
+  const T* krow = static_cast<const T*>(a.k.p) + b * a.k.sb + s * a.k.ss;
+  const T* vrow = static_cast<const T*>(a.v.p) + s * a.v.ss;
+  T* qdst = static_cast<T*>(a.qo.p) + b * a.qo.sb + s * a.qo.ss;
+  T* kodst = PAGED ? static_cast<T*>(a.kc) + kdst : static_cast<T*>(a.ko.p) + b * a.ko.sb + s * a.ko.ss;
+  T* vodst = static_cast<T*>(a.vc) + vdst;
+  const int64_t kosh = PAGED ? a.kh : a.ko.sh;
+  const bool put_k = PAGED ? put : live;
+
+  float wa[4], wb[4];
+  bool q_weight = h_begin < a.Hq;
+  load_weight<T, D, INTER>(q_weight ? a.qw : a.kw, a.w_f32, l, wa, wb);
+#pragma unroll 1
+  for (int h0 = h_begin; h0 < h_end; h0 += kUnroll) {
+    Raw<T> raw[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int h = h0 + u;
+      const T* row = h < a.Hq ? qrow + h * a.q.sh
+                              : (h < a.Hq + a.Hkv ? krow + (h - a.Hq) * a.k.sh
+                                                  : vrow + (h - a.Hq - a.Hkv) * a.v.sh);
+      if (live && h < h_end) raw[u] = load_row<T, D, INTER>(row, l);
+      else raw[u] = Raw<T>{};
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int h = h0 + u;
+      float x[4], y[4];
+      to_pairs<T, INTER>(raw[u], x, y);
+      if (PAGED && h >= a.Hq + a.Hkv) {  // a value: copied (the conversion there and back is exact)
+        if (put && h < h_end)
+          store_row<T, D, INTER>(vodst + (h - a.Hq - a.Hkv) * a.vh, l, x, y);
+        continue;
+      }
+      if (q_weight && h >= a.Hq) {
+        load_weight<T, D, INTER>(a.kw, a.w_f32, l, wa, wb);
+        q_weight = false;
+      }
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
+      const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + a.eps);
+      float o0[4], o1[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float ya = x[i] * r * wa[i], yb = y[i] * r * wb[i];
+        o0[i] = ya * c[i] - yb * sn[i];
+        o1[i] = ya * sn[i] + yb * c[i];
+      }
+      if (h < h_end) {
+        if (h < a.Hq) {
+          if (live) store_row<T, D, INTER>(qdst + h * a.qo.sh, l, o0, o1);
+        } else if (put_k) {
+          store_row<T, D, INTER>(kodst + (h - a.Hq) * kosh, l, o0, o1);
+        }
+      }
+    }
+  }
+}
+
+struct NormBackArgs {
+  HeadsIn x[2], dy[2];  // queries, keys
+  HeadsOut dx[2];
+  int B, S, Hq, Hkv;
+  int per_group, head_runs;
+  const void* w[2];
+  int w_f32;
+  const float *cos, *sin;
+  int n_pos;
+  const int32_t* positions;
+  int64_t pos_b;
+  float eps;
+  float* part;  // (CTAs, 2, D) weight-gradient sums
+};
+
+// Units (token group, run of per_group heads) are taken in a fixed stride over the grid, so
+// a CTA's share of the weight sums, and the order inside it, depend on the sizes alone.
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(kNormThreads) norm_rotation_back_kernel(const NormBackArgs a) {
+  constexpr int L = D / 8, kGroups = kNormThreads / L;
+  constexpr int kUnroll = 2;
+  const int l = threadIdx.x % L, grp = threadIdx.x / L;
+  const int64_t ntok = static_cast<int64_t>(a.B) * a.S;
+  const int64_t tgroups = (ntok + kGroups - 1) / kGroups;
+  const int heads = a.Hq + a.Hkv;
+  float dwa[2][4] = {}, dwb[2][4] = {};
+  float wa[2][4], wb[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) load_weight<T, D, INTER>(a.w[i], a.w_f32, l, wa[i], wb[i]);
+#pragma unroll 1
+  for (int64_t u = blockIdx.x; u < tgroups * a.head_runs; u += gridDim.x) {
+    const int64_t tok = (u / a.head_runs) * kGroups + grp;
+    const int run = static_cast<int>(u % a.head_runs);
+    const bool in = tok < ntok;
+    const int b = in ? static_cast<int>(tok / a.S) : 0, s = in ? static_cast<int>(tok % a.S) : 0;
+    int pos = in ? checked_position(a.positions, a.pos_b, b, s, a.n_pos) : -1;
+    if (pos == -2 && l == 0) report_device_error(kStatusBadLabel, kNormSite + 2);
+    const bool live = pos >= 0;
+    if (pos < 0) pos = 0;
+    float c[4] = {}, sn[4] = {};
+    if (live) {
+      const float4 c4 = *reinterpret_cast<const float4*>(a.cos + static_cast<int64_t>(pos) * (D / 2) + 4 * l);
+      const float4 s4 = *reinterpret_cast<const float4*>(a.sin + static_cast<int64_t>(pos) * (D / 2) + 4 * l);
+      c[0] = c4.x; c[1] = c4.y; c[2] = c4.z; c[3] = c4.w;
+      sn[0] = s4.x; sn[1] = s4.y; sn[2] = s4.z; sn[3] = s4.w;
+    }
+    const int h_begin = run * a.per_group, h_end = min(heads, h_begin + a.per_group);
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {  // queries, then keys of the run
+      const int lo = side ? max(h_begin, a.Hq) - a.Hq : h_begin;
+      const int hi = side ? h_end - a.Hq : min(h_end, a.Hq);
+      const T* xrow = static_cast<const T*>(a.x[side].p) + b * a.x[side].sb + s * a.x[side].ss;
+      const T* grow = static_cast<const T*>(a.dy[side].p) + b * a.dy[side].sb + s * a.dy[side].ss;
+      T* drow = static_cast<T*>(a.dx[side].p) + b * a.dx[side].sb + s * a.dx[side].ss;
+#pragma unroll 1
+      for (int h0 = lo; h0 < hi; h0 += kUnroll) {
+        Raw<T> rx[kUnroll], rg[kUnroll];
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) {
+          rx[j] = rg[j] = Raw<T>{};
+          if (live && h0 + j < hi) {
+            rx[j] = load_row<T, D, INTER>(xrow + (h0 + j) * a.x[side].sh, l);
+            rg[j] = load_row<T, D, INTER>(grow + (h0 + j) * a.dy[side].sh, l);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) {
+          float xa[4], xb[4], ga[4], gb[4], za[4], zb[4];
+          to_pairs<T, INTER>(rx[j], xa, xb);
+          to_pairs<T, INTER>(rg[j], ga, gb);
+          float ss = 0.f, dot = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            za[i] = ga[i] * c[i] + gb[i] * sn[i];
+            zb[i] = gb[i] * c[i] - ga[i] * sn[i];
+            ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
+            dot = fmaf(za[i] * wa[side][i], xa[i], fmaf(zb[i] * wb[side][i], xb[i], dot));
+          }
+          ss = row_sum<D>(ss);
+          dot = row_sum<D>(dot);
+          const float r = rsqrtf(ss * (1.f / D) + a.eps);
+          const float k = r * r * dot * (1.f / D);
+          float oa[4], ob[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            dwa[side][i] = fmaf(za[i] * r, xa[i], dwa[side][i]);
+            dwb[side][i] = fmaf(zb[i] * r, xb[i], dwb[side][i]);
+            oa[i] = r * (za[i] * wa[side][i] - xa[i] * k);
+            ob[i] = r * (zb[i] * wb[side][i] - xb[i] * k);
+          }
+          if (in && h0 + j < hi) {
+            if (!live) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) oa[i] = ob[i] = 0.f;
+            }
+            store_row<T, D, INTER>(drow + (h0 + j) * a.dx[side].sh, l, oa, ob);
+          }
+        }
+      }
+    }
+  }
+  // the lane groups' sums, added in group order
+  __shared__ float red[kGroups][2][D];
+#pragma unroll
+  for (int side = 0; side < 2; ++side)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int da = INTER ? 8 * l + 2 * i : 4 * l + i;
+      const int db = INTER ? da + 1 : D / 2 + 4 * l + i;
+      red[grp][side][da] = dwa[side][i];
+      red[grp][side][db] = dwb[side][i];
+    }
+  __syncthreads();
+  for (int e = threadIdx.x; e < 2 * D; e += kNormThreads) {
+    float t = 0.f;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) t += red[g][e / D][e % D];
+    a.part[static_cast<size_t>(blockIdx.x) * 2 * D + e] = t;
+  }
+}
+
+// Sum of the CTAs' shares, one CTA per 32 columns of the (2, D) sums: warp w adds shares
+// w, w + 32, ... and the warps' sums are added in order, in fp64 (hundreds of shares with
+// cancelling signs).
+__global__ void __launch_bounds__(1024) norm_weight_sum_kernel(const float* __restrict__ part,
+                                                               int n, int D, float* __restrict__ dqw,
+                                                               float* __restrict__ dkw) {
+  __shared__ double red[32][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;
+  double t = 0.0;
+#pragma unroll 4
+  for (int i = w; i < n; i += 32) t += static_cast<double>(part[static_cast<size_t>(i) * 2 * D + col]);
+  red[w][lane] = t;
+  __syncthreads();
+  if (w == 0) {
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s += red[i][lane];
+    (col < D ? dqw[col] : dkw[col - D]) = static_cast<float>(s);
+  }
+}
+
+int norm_elem_bytes(int dtype) { return dtype == BSA_F32 ? 4 : 2; }
+
+int check_heads(const bsa_heads& h, int dtype, const char* name) {
+  if (!h.ptr) return fail(BSA_ERR_INVALID_ARG, "%s is null", name);
+  const int unit = 16 / norm_elem_bytes(dtype);
+  if (reinterpret_cast<uintptr_t>(h.ptr) % 16 || h.stride_b % unit || h.stride_h % unit ||
+      h.stride_s % unit)
+    return fail(BSA_ERR_INVALID_ARG, "%s: pointer or strides not multiples of 16 bytes", name);
+  return BSA_OK;
+}
+
+int check_norm_common(const bsa_shape& s, const void* qw, const void* kw, const float* cos,
+                      const float* sin, int n_pos, float eps) {
+  if (s.dtype != BSA_BF16 && s.dtype != BSA_F16 && s.dtype != BSA_F32)
+    return fail(BSA_ERR_UNSUPPORTED, "dtype %d", s.dtype);
+  if (s.D != 64 && s.D != 128) return fail(BSA_ERR_UNSUPPORTED, "head dim %d not in {64,128}", s.D);
+  if (s.B < 0 || s.Sq < 0 || s.Hq <= 0 || s.Hkv <= 0 || s.Sq != s.Sk)
+    return fail(BSA_ERR_INVALID_ARG, "bad shape");
+  if (s.Hq > 16384 || s.Hkv > 16384) return fail(BSA_ERR_UNSUPPORTED, "more than 16384 heads");
+  if (static_cast<int64_t>(s.B) * s.Sq > INT32_MAX)
+    return fail(BSA_ERR_UNSUPPORTED, "B*S exceeds 2^31 - 1");
+  if (!(eps >= 0.f)) return fail(BSA_ERR_INVALID_ARG, "eps < 0");
+  if (!qw || !kw || !cos || !sin) return fail(BSA_ERR_INVALID_ARG, "null pointer");
+  if (n_pos < 0) return fail(BSA_ERR_INVALID_ARG, "n_pos < 0");
+  if (reinterpret_cast<uintptr_t>(cos) % 16 || reinterpret_cast<uintptr_t>(sin) % 16)
+    return fail(BSA_ERR_INVALID_ARG, "cos and sin must be 16-byte aligned");
+  return BSA_OK;
+}
+
+HeadsIn in_of(const bsa_heads& h) { return {h.ptr, h.stride_b, h.stride_h, h.stride_s}; }
+HeadsOut out_of(const bsa_heads& h) { return {h.ptr, h.stride_b, h.stride_h, h.stride_s}; }
+
+// Heads per lane group: a group walks over all heads of its token when the tokens alone
+// fill the GPU several times over, and over fewer, in whole steps of 4, when they do not.
+int heads_per_group(int64_t token_groups, int heads) {
+  constexpr int64_t kWant = 148 * 16;  // CTAs that keep every SM's loads in flight twice over
+  const int64_t runs = std::min<int64_t>((heads + 3) / 4, std::max<int64_t>(1, kWant / std::max<int64_t>(token_groups, 1)));
+  return static_cast<int>(((heads + runs - 1) / runs + 3) / 4 * 4);
+}
+
+template <typename T, int D, bool PAGED>
+void launch_norm_t(const NormArgs& a, dim3 grid, int interleaved, cudaStream_t st) {
+  if (interleaved) norm_rotation_kernel<T, D, true, PAGED><<<grid, kNormThreads, 0, st>>>(a);
+  else norm_rotation_kernel<T, D, false, PAGED><<<grid, kNormThreads, 0, st>>>(a);
+}
+
+template <bool PAGED>
+int launch_norm(NormArgs& a, int dtype, int D, int interleaved, cudaStream_t st) {
+  const int64_t ntok = static_cast<int64_t>(a.B) * a.S;
+  const int per_cta = kNormThreads / (D / 8);
+  const int64_t tg = (ntok + per_cta - 1) / per_cta;
+  a.per_group = heads_per_group(tg, a.heads);
+  const dim3 grid(static_cast<unsigned>(tg), ceil_div(a.heads, a.per_group));
+#define BSA_NORM(T)                                                              \
+  (D == 64 ? launch_norm_t<T, 64, PAGED>(a, grid, interleaved, st)               \
+           : launch_norm_t<T, 128, PAGED>(a, grid, interleaved, st))
+  if (dtype == BSA_BF16) BSA_NORM(__nv_bfloat16);
+  else if (dtype == BSA_F16) BSA_NORM(__half);
+  else if constexpr (!PAGED) BSA_NORM(float);
+#undef BSA_NORM
+  count_launch();
+  return check_cuda(cudaGetLastError(), "norm_rotation_kernel");
+}
+
+// CTAs of the backward pass: each leaves one share of the weight sums.
+int norm_back_ctas(const bsa_shape& s, int* per_group, int* head_runs) {
+  const int per_cta = kNormThreads / (s.D / 8);
+  const int64_t tg = (static_cast<int64_t>(s.B) * s.Sq + per_cta - 1) / per_cta;
+  *per_group = heads_per_group(tg, s.Hq + s.Hkv);
+  *head_runs = ceil_div(s.Hq + s.Hkv, *per_group);
+  return static_cast<int>(std::min<int64_t>(148 * 4, std::max<int64_t>(tg * *head_runs, 1)));
+}
+
+}  // namespace
+
+}  // namespace bsa
+
+extern "C" {
+
+int bsa_qk_norm_rotation(bsa_heads q, bsa_heads k, bsa_shape shape, const void* q_weight,
+                         const void* k_weight, int weight_f32, const float* cos, const float* sin,
+                         int n_pos, const int32_t* positions, int64_t pos_b_stride, float eps,
+                         int interleaved, bsa_heads q_out, bsa_heads k_out, void* stream) {
+  using namespace bsa;
+  int st = check_norm_common(shape, q_weight, k_weight, cos, sin, n_pos, eps);
+  if (st != BSA_OK) return st;
+  if (static_cast<int64_t>(shape.B) * shape.Sq == 0) return BSA_OK;
+  if ((st = check_heads(q, shape.dtype, "q")) || (st = check_heads(k, shape.dtype, "k")) ||
+      (st = check_heads(q_out, shape.dtype, "q_out")) || (st = check_heads(k_out, shape.dtype, "k_out")))
+    return st;
+  if (!positions && shape.Sq > n_pos)
+    return fail(BSA_ERR_INVALID_ARG, "%d tokens, %d positions in the table", shape.Sq, n_pos);
+  NormArgs a{};
+  a.q = in_of(q);
+  a.k = in_of(k);
+  a.qo = out_of(q_out);
+  a.ko = out_of(k_out);
+  a.B = shape.B;
+  a.S = shape.Sq;
+  a.Hq = shape.Hq;
+  a.Hkv = shape.Hkv;
+  a.heads = shape.Hq + shape.Hkv;
+  a.qw = q_weight;
+  a.kw = k_weight;
+  a.w_f32 = weight_f32;
+  a.cos = cos;
+  a.sin = sin;
+  a.n_pos = n_pos;
+  a.positions = positions;
+  a.pos_b = pos_b_stride;
+  a.eps = eps;
+  return launch_norm<false>(a, shape.dtype, shape.D, interleaved, as_stream(stream));
+}
+
+size_t bsa_qk_norm_rotation_workspace_bytes(bsa_shape shape) {
+  if ((shape.D != 64 && shape.D != 128) || shape.B < 0 || shape.Sq < 0 || shape.Hq <= 0 ||
+      shape.Hkv <= 0 || shape.Hq > 16384 || shape.Hkv > 16384)
+    return 0;
+  int pg, hr;
+  return bsa::align_up(static_cast<size_t>(bsa::norm_back_ctas(shape, &pg, &hr)) * 2 * shape.D *
+                           sizeof(float), 256);
+}
+
+int bsa_qk_norm_rotation_backward(bsa_heads dq_out, bsa_heads dk_out, bsa_heads q, bsa_heads k,
+                                  bsa_shape shape, const void* q_weight, const void* k_weight,
+                                  int weight_f32, const float* cos, const float* sin, int n_pos,
+                                  const int32_t* positions, int64_t pos_b_stride, float eps,
+                                  int interleaved, bsa_heads dq, bsa_heads dk, float* dq_weight,
+                                  float* dk_weight, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  using namespace bsa;
+  int st = check_norm_common(shape, q_weight, k_weight, cos, sin, n_pos, eps);
+  if (st != BSA_OK) return st;
+  if (!dq_weight || !dk_weight) return fail(BSA_ERR_INVALID_ARG, "null weight gradient");
+  const bool none = static_cast<int64_t>(shape.B) * shape.Sq == 0;
+  if (!none) {
+    if ((st = check_heads(dq_out, shape.dtype, "dq_out")) || (st = check_heads(dk_out, shape.dtype, "dk_out")) ||
+        (st = check_heads(q, shape.dtype, "q")) || (st = check_heads(k, shape.dtype, "k")) ||
+        (st = check_heads(dq, shape.dtype, "dq")) || (st = check_heads(dk, shape.dtype, "dk")))
+      return st;
+    if (!positions && shape.Sq > n_pos)
+      return fail(BSA_ERR_INVALID_ARG, "%d tokens, %d positions in the table", shape.Sq, n_pos);
+  }
+  if (!workspace || workspace_bytes < bsa_qk_norm_rotation_workspace_bytes(shape))
+    return fail(BSA_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes,
+                bsa_qk_norm_rotation_workspace_bytes(shape));
+  NormBackArgs a{};
+  a.x[0] = in_of(q);
+  a.x[1] = in_of(k);
+  a.dy[0] = in_of(dq_out);
+  a.dy[1] = in_of(dk_out);
+  a.dx[0] = out_of(dq);
+  a.dx[1] = out_of(dk);
+  a.B = shape.B;
+  a.S = shape.Sq;
+  a.Hq = shape.Hq;
+  a.Hkv = shape.Hkv;
+  a.w[0] = q_weight;
+  a.w[1] = k_weight;
+  a.w_f32 = weight_f32;
+  a.cos = cos;
+  a.sin = sin;
+  a.n_pos = n_pos;
+  a.positions = positions;
+  a.pos_b = pos_b_stride;
+  a.eps = eps;
+  a.part = static_cast<float*>(workspace);
+  const int ctas = none ? 0 : norm_back_ctas(shape, &a.per_group, &a.head_runs);
+  cudaStream_t cs = as_stream(stream);
+  if (!none) {
+#define BSA_NORM_BACK(T)                                                                        \
+  (shape.D == 64                                                                                \
+       ? (interleaved ? norm_rotation_back_kernel<T, 64, true><<<ctas, kNormThreads, 0, cs>>>(a)   \
+                      : norm_rotation_back_kernel<T, 64, false><<<ctas, kNormThreads, 0, cs>>>(a)) \
+       : (interleaved ? norm_rotation_back_kernel<T, 128, true><<<ctas, kNormThreads, 0, cs>>>(a)  \
+                      : norm_rotation_back_kernel<T, 128, false><<<ctas, kNormThreads, 0, cs>>>(a)))
+    if (shape.dtype == BSA_BF16) BSA_NORM_BACK(__nv_bfloat16);
+    else if (shape.dtype == BSA_F16) BSA_NORM_BACK(__half);
+    else BSA_NORM_BACK(float);
+#undef BSA_NORM_BACK
+    count_launch();
+    if ((st = check_cuda(cudaGetLastError(), "norm_rotation_back_kernel")) != BSA_OK) return st;
+  }
+  norm_weight_sum_kernel<<<2 * shape.D / 32, 1024, 0, cs>>>(a.part, ctas, shape.D, dq_weight, dk_weight);
+  count_launch();
+  return check_cuda(cudaGetLastError(), "norm_weight_sum_kernel");
+}
+
+int bsa_paged_qk_norm_append(bsa_heads q, bsa_heads k, bsa_heads v, int T, int Hq,
+                             const void* q_weight, const void* k_weight, int weight_f32,
+                             const float* cos, const float* sin, int n_pos,
+                             const int32_t* positions, const int32_t* slots, float eps,
+                             int interleaved, bsa_heads q_out, bsa_paged_cache cache,
+                             void* stream) {
+  using namespace bsa;
+  int st = check_paged_cache(cache);
+  if (st != BSA_OK) return st;
+  const bsa_shape shape{1, Hq, cache.Hkv, T, T, cache.D, cache.dtype};
+  if ((st = check_norm_common(shape, q_weight, k_weight, cos, sin, n_pos, eps)) != BSA_OK) return st;
+  if (T == 0) return BSA_OK;
+  if (!positions || !slots) return fail(BSA_ERR_INVALID_ARG, "positions or slots is null");
+  q.stride_b = k.stride_b = v.stride_b = q_out.stride_b = 0;
+  if ((st = check_heads(q, cache.dtype, "q")) || (st = check_heads(k, cache.dtype, "k")) ||
+      (st = check_heads(v, cache.dtype, "v")) || (st = check_heads(q_out, cache.dtype, "q_out")))
+    return st;
+  NormArgs a{};
+  a.q = in_of(q);
+  a.k = in_of(k);
+  a.v = in_of(v);
+  a.qo = out_of(q_out);
+  a.B = 1;
+  a.S = T;
+  a.Hq = Hq;
+  a.Hkv = cache.Hkv;
+  a.heads = Hq + 2 * cache.Hkv;
+  a.qw = q_weight;
+  a.kw = k_weight;
+  a.w_f32 = weight_f32;
+  a.cos = cos;
+  a.sin = sin;
+  a.n_pos = n_pos;
+  a.positions = positions;
+  a.eps = eps;
+  a.slots = slots;
+  a.kc = cache.k;
+  a.vc = cache.v;
+  a.kp = cache.k_page_stride;
+  a.kh = cache.k_head_stride;
+  a.kr = cache.k_row_stride;
+  a.vp = cache.v_page_stride;
+  a.vh = cache.v_head_stride;
+  a.vr = cache.v_row_stride;
+  a.page_shift = __builtin_ctz(cache.page);
+  a.n_slots = cache.n_pages * cache.page;
+  return launch_norm<true>(a, cache.dtype, cache.D, interleaved, as_stream(stream));
+}
+
+}  // extern "C"

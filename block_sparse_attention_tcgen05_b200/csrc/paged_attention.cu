@@ -1,0 +1,1196 @@
+// Attention of every request's new tokens over its paged cache, block-sparse at page
+// granularity. The rows of one (request, KV head) are its tokens times the G query heads of
+// the KV head (row = token * G + head), so a key is read once for all heads that share it.
+// Two kernels split the requests by that row count:
+//
+//   paged_token_kernel  at most kTokenRows rows (a step of single or few tokens). Bound by the
+//       cache's bytes: keys and values go from global memory straight into the registers
+//       that the matrix instruction takes, 16 keys at a time, with no shared memory on the
+//       way. The (request, head, 64-key chunk) space is cut into equal contiguous spans, one
+//       per CTA, so ragged lengths balance; a (request, head) that crosses a span border
+//       leaves partial results that token_combine_kernel joins.
+//   paged_tile_kernel   more rows. tcgen05: two 128-row tiles per CTA over 128-key chunks
+//       gathered page by page with TMA, logits and weights in TMEM, one softmax thread per
+//       row. With few tiles the key range is split over CTAs and tile_combine_kernel joins.
+//
+// Both keep the running maximum and sum of a softmax in fp32, in base-2 units.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace bsa {
+
+namespace {
+
+constexpr int kTokenRows = 16;      // rows per (request, KV head) of the token kernel
+constexpr int kPagedMaxR = 4096;    // requests of one call
+constexpr int kPagedSite = 140;
+
+struct PagedArgs {
+  const void* q;
+  int64_t qh, qt;
+  const void *kc, *vc;
+  int64_t kp, kh, kr, vp, vh, vr;
+  int n_pages, page_shift, Hkv, G, T, R;
+  const int32_t* table;
+  int width;
+  int64_t table_stride;
+  const int32_t *cu, *ctx;
+  const uint8_t* mask;
+  int64_t mr, mg;
+  float scale_log2;
+  int causal;
+  void* out;
+  int64_t oh, ot;
+  int max_new;   // host bound of new tokens per request
+  int min_rows;  // requests of at most this many rows belong to the token kernel
+  float* part;
+  int splits;      // tile kernel: CTAs per tile pair over its keys
+  int units_max;   // tile kernel: bound of tile pairs per KV head
+  int workers;     // token kernel: CTAs
+  int tok_rows;    // token kernel: rows of a request that its instance holds (8 or 16)
+  int one_each;    // token kernel: one CTA per (request, KV head), nothing to join
+};
+
+// A request's lengths, made safe against any device contents: token range inside [0, T),
+// context inside the table's reach.
+struct Request {
+  int t0, n;    // first token, tokens
+  int ctx, len; // cached tokens before, keys in all
+};
+
+__device__ __forceinline__ Request load_request(const PagedArgs& a, int r) {
+  Request q;
+  const int t0 = a.cu[r], t1 = a.cu[r + 1];
+  q.t0 = min(max(t0, 0), a.T);
+  q.n = max(min(t1, a.T) - q.t0, 0);
+  const int64_t reach = static_cast<int64_t>(a.width) << a.page_shift;
+  const int64_t c = max(a.ctx[r], 0);
+  q.ctx = static_cast<int>(min(c, reach));
+  q.len = static_cast<int>(min(c + q.n, reach));
+  return q;
+}
+
+__device__ __forceinline__ void check_request(const PagedArgs& a, int r) {
+  const int64_t reach = static_cast<int64_t>(a.width) << a.page_shift;
+  const int t0 = a.cu[r], t1 = a.cu[r + 1], c = a.ctx[r];
+  const bool ok = t0 >= 0 && t1 >= t0 && t1 <= a.T && c >= 0 && t1 - t0 <= a.max_new &&
+                  (t1 == t0 || static_cast<int64_t>(c) + (t1 - t0) <= reach);
+  if (!ok) report_device_error(kStatusBadLabel, kPagedSite);
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
+  if constexpr (std::is_same<T, __half>::value) {
+    __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
+  } else {
+    __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+}
+
+// ================================================================ token kernel
+constexpr int kTokWarps = 4;
+constexpr int kTokThreads = 32 * kTokWarps;
+constexpr int kTokChunk = 64;     // keys of a work unit: one 16-key block per warp
+constexpr int kTokMinSpan = 4;    // units a CTA takes at least
+
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+      : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+      : "l"(p));
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
+  return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
+}
+
+// Chunks of 64 keys of request r that the token kernel takes (0 for one of the tile kernel's).
+__device__ __forceinline__ int token_chunks(const PagedArgs& a, const Request& q) {
+  if (q.n <= 0 || q.n * static_cast<int64_t>(a.G) > a.tok_rows) return 0;
+  return (q.len + kTokChunk - 1) / kTokChunk;
+}
+
+// The unit space: request-major, then KV head, then chunk; CTA w takes [w*span, (w+1)*span).
+__device__ __forceinline__ int64_t token_span(int64_t units, int workers) {
+  const int64_t s = (units + workers - 1) / workers;
+  return s < kTokMinSpan ? kTokMinSpan : s;
+}
+
+// Partial results: two slots per CTA (0: a (request, head) that began before its span, 1: one
+// that goes on behind it), each O (kTokenRows x D) unnormalised, then (max, sum) pairs.
+__device__ __forceinline__ float* token_slot(const PagedArgs& a, int w, int slot, int D) {
+  return a.part + (static_cast<size_t>(w) * 2 + slot) * kTokenRows * (D + 2);
+}
+
+// One warp's share of a (request, head): S^T = K Q^T with 16 keys as the M side and 8 rows
+// as the N side, then O^T = V^T P^T. A lane (g = lane / 4, c = lane % 4) holds 16-byte pieces
+// of keys g and g + 8 for the first product (the order of D inside a product is free, so a
+// piece serves two K-steps), and of keys 2c, 2c+1, 2c+8, 2c+9 for the second, whose pairs of
+// neighbouring keys are interleaved with byte permutes; the weights reach their second
+// product's lane with one 8x8 transposition.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kTokThreads) paged_token_kernel(const PagedArgs a) {
+  constexpr int KC = D / 32;  // 16-byte pieces of a key per lane (first product)
+  constexpr int VC = D / 64;  // 16-byte pieces of a value row per lane (second product)
+  constexpr int MT = D / 16;  // 16-wide slices of D in the second product
+  extern __shared__ int32_t s_units[];  // prefix of units per KV head: R + 1 entries
+  __shared__ float s_o[kTokWarps][8 * NT][D + 4];
+  __shared__ float s_m[kTokWarps][8 * NT], s_l[kTokWarps][8 * NT];
+  __shared__ int s_warp[kTokWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+
+  int64_t u_begin, u_end;
+  if (a.one_each) {
+    if (tid == 0) check_request(a, blockIdx.x / a.Hkv);
+    u_begin = 0;
+    u_end = 1;
+  } else {
+    int base = 0;
+    for (int r0 = 0; r0 < a.R; r0 += kTokThreads) {
+      const int r = r0 + tid;
+      int n = 0;
+      if (r < a.R) {
+        if (blockIdx.x == 0) check_request(a, r);
+        n = token_chunks(a, load_request(a, r));
+      }
+      int incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) s_warp[warp] = incl;
+      __syncthreads();
+      int b = base;
+#pragma unroll
+      for (int w = 0; w < kTokWarps; ++w) {
+        if (w < warp) b += s_warp[w];
+        base += s_warp[w];
+      }
+      if (r < a.R) s_units[r] = b + incl - n;
+      __syncthreads();
+    }
+    if (tid == 0) s_units[a.R] = base;
+    __syncthreads();
+    const int64_t units = static_cast<int64_t>(base) * a.Hkv;
+    const int64_t span = token_span(units, a.workers);
+    u_begin = span * blockIdx.x;
+    u_end = min(units, u_begin + span);
+  }
+
+  for (int64_t u = u_begin; u < u_end;) {
+    // the (request, head) of unit u and the chunks of it that lie in this span
+    int r, h, ch0, ch1, nch;
+    if (a.one_each) {
+      r = blockIdx.x / a.Hkv;
+      h = blockIdx.x % a.Hkv;
+      ch0 = 0;
+      ch1 = nch = token_chunks(a, load_request(a, r));
+      u = u_end;
+      if (nch == 0) break;
+    } else {
+      int lo = 0, hi = a.R - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (static_cast<int64_t>(s_units[mid]) * a.Hkv <= u) lo = mid;
+        else hi = mid - 1;
+      }
+      r = lo;
+      nch = s_units[r + 1] - s_units[r];
+      const int64_t in = u - static_cast<int64_t>(s_units[r]) * a.Hkv;
+      h = static_cast<int>(in / nch);
+      ch0 = static_cast<int>(in % nch);
+      ch1 = static_cast<int>(min(static_cast<int64_t>(nch), ch0 + (u_end - u)));
+      u += ch1 - ch0;
+    }
+    const Request q = load_request(a, r);
+    const int rows = q.n * a.G;
+
+    // Q: row 8 nt + g of the group, pieces of 8 values at 32 j + 8 c
+    uint4 qf[NT][KC];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = 8 * nt + g;
+#pragma unroll
+      for (int j = 0; j < KC; ++j) qf[nt][j] = make_uint4(0, 0, 0, 0);
+      if (row < rows) {
+        const T* p = static_cast<const T*>(a.q) + (static_cast<int64_t>(h) * a.G + row % a.G) * a.qh +
+                     static_cast<int64_t>(q.t0 + row / a.G) * a.qt;
+#pragma unroll
+        for (int j = 0; j < KC; ++j) qf[nt][j] = ldg_stream(p + 32 * j + 8 * c);
+      }
+    }
+    // last key that the lane's two softmax rows (2c, 2c + 1 of each 8) see
+    int lim[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = 8 * nt + 2 * c + i;
+        lim[nt][i] = row < rows ? min(a.causal ? q.ctx + row / a.G : q.len - 1, q.len - 1) : -1;
+      }
+    const int lim_all = a.causal ? min(q.ctx, q.len - 1) : q.len - 1;  // keys every row sees
+
+    float m[NT][2], l[NT][2], o[MT][NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[t][nt][i] = 0.f;
+    }
+
+    const T* kbase = static_cast<const T*>(a.kc) + h * a.kh;
+    const T* vbase = static_cast<const T*>(a.vc) + h * a.vh;
+    const int32_t* trow = a.table + r * a.table_stride;
+    const uint8_t* mrow = a.mask ? a.mask + r * a.mr + h * a.mg : nullptr;
+    const int blk_end = min(ch1 * (kTokChunk / 16), (q.len + 15) >> 4);
+    const int bpp_shift = a.page_shift - 4;  // 16-key blocks per page
+    // page of a block, -1 where there is nothing to read
+    auto page_of = [&](int blk) -> int {
+      if (blk >= blk_end) return -1;
+      const int pg = blk >> bpp_shift;
+      if (mrow && !mrow[pg]) return -1;
+      const int id = trow[pg];
+      if (id < 0 || id >= a.n_pages) {
+        if (lane == 0) report_device_error(kStatusBadLabel, kPagedSite + 1);
+        return -1;
+      }
+      return id;
+    };
+    uint4 kf[2][KC], vf[4][VC];
+    auto load_k = [&](int id, int blk) {
+      const int row0 = (blk << 4) & ((1 << a.page_shift) - 1);
+      const T* p = kbase + static_cast<int64_t>(id) * a.kp + static_cast<int64_t>(row0) * a.kr + 8 * c;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool in = (blk << 4) + g + 8 * i < q.len;
+#pragma unroll
+        for (int j = 0; j < KC; ++j)
+          kf[i][j] = in ? ldg_stream(p + (g + 8 * i) * a.kr + 32 * j) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto load_v = [&](int id, int blk) {
+      const int row0 = (blk << 4) & ((1 << a.page_shift) - 1);
+      const T* p = vbase + static_cast<int64_t>(id) * a.vp + static_cast<int64_t>(row0) * a.vr + 8 * g;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = 2 * c + (i & 1) + 8 * (i >> 1);
+        const bool in = (blk << 4) + key < q.len;  // rows behind the last key count as zeros
+#pragma unroll
+        for (int j = 0; j < VC; ++j)
+          vf[i][j] = in ? ldg_stream(p + key * a.vr + 64 * j) : make_uint4(0, 0, 0, 0);
+      }
+    };
+
+    int blk = ch0 * (kTokChunk / 16) + warp;
+    int id = page_of(blk), id_next = page_of(blk + kTokWarps);
+    if (id >= 0) {
+      load_k(id, blk);
+      load_v(id, blk);
+    }
+#pragma unroll 1
+    for (; blk < blk_end; blk += kTokWarps) {
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+        if (id >= 0) {
+#pragma unroll
+          for (int j = 0; j < KC; ++j) {
+            mma_16816<T>(s[nt], kf[0][j].x, kf[1][j].x, kf[0][j].y, kf[1][j].y, qf[nt][j].x, qf[nt][j].y);
+            mma_16816<T>(s[nt], kf[0][j].z, kf[1][j].z, kf[0][j].w, kf[1][j].w, qf[nt][j].z, qf[nt][j].w);
+          }
+        }
+      }
+      // the next block's keys are on their way during this block's softmax
+      if (id_next >= 0) load_k(id_next, blk + kTokWarps);
+      const int id_after = page_of(blk + 2 * kTokWarps);
+      if (id >= 0) {
+        const int key = (blk << 4) + g;
+        const bool edge = (blk << 4) + 15 > lim_all;
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] = s[nt][i] * a.scale_log2;
+            if (edge && key + 8 * (i >> 1) > lim[nt][i & 1]) x[i] = -INFINITY;
+          }
+          float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
+          }
+          // The running maximum moves only when it is passed by more than 8 (weights stay
+          // below 2^8), so the accumulators are rarely rescaled.
+          const bool need = mx0 > m[nt][0] + 8.f || mx1 > m[nt][1] + 8.f;
+          if (__any_sync(0xffffffffu, need)) {
+            const float n0 = fmaxf(m[nt][0], mx0), n1 = fmaxf(m[nt][1], mx1);
+            const float f0 = n0 == -INFINITY ? 1.f : ex2(m[nt][0] - n0);
+            const float f1 = n1 == -INFINITY ? 1.f : ex2(m[nt][1] - n1);
+            m[nt][0] = n0;
+            m[nt][1] = n1;
+            l[nt][0] *= f0;
+            l[nt][1] *= f1;
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+              o[t][nt][0] *= f0;
+              o[t][nt][1] *= f1;
+              o[t][nt][2] *= f0;
+              o[t][nt][3] *= f1;
+            }
+          }
+          const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+          const float b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+          const float p0 = ex2(x[0] - b0), p1 = ex2(x[1] - b1), p2 = ex2(x[2] - b0), p3 = ex2(x[3] - b1);
+          l[nt][0] += p0 + p2;
+          l[nt][1] += p1 + p3;
+          pb[nt][0] = transpose8x8(pack_pair<T>(p0, p1));
+          pb[nt][1] = transpose8x8(pack_pair<T>(p2, p3));
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          const int j = t / 4, w = t % 4;
+          const uint32_t k0 = word_of(vf[0][j], w), k1 = word_of(vf[1][j], w);
+          const uint32_t k8 = word_of(vf[2][j], w), k9 = word_of(vf[3][j], w);
+          const uint32_t a0 = __byte_perm(k0, k1, 0x5410), a1 = __byte_perm(k0, k1, 0x7632);
+          const uint32_t a2 = __byte_perm(k8, k9, 0x5410), a3 = __byte_perm(k8, k9, 0x7632);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_16816<T>(o[t][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+        }
+      }
+      if (id_next >= 0) load_v(id_next, blk + kTokWarps);
+      id = id_next;
+      id_next = id_after;
+    }
+
+    // the warps' results of this (request, head) joined through shared memory
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], d);
+        if (g == 0) {
+          s_m[warp][8 * nt + 2 * c + i] = m[nt][i];
+          s_l[warp][8 * nt + 2 * c + i] = l[nt][i];
+        }
+      }
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int d = (t / 4) * 64 + 8 * g + 2 * (t % 4);
+          *reinterpret_cast<float2*>(&s_o[warp][8 * nt + 2 * c + i][d]) =
+              make_float2(o[t][nt][i], o[t][nt][i + 2]);
+        }
+    __syncthreads();
+    const bool whole = ch0 == 0 && ch1 == nch;
+    float* slot = whole ? nullptr : token_slot(a, blockIdx.x, ch0 == 0 ? 1 : 0, D);
+    for (int e = tid; e < rows * (D / 2); e += kTokThreads) {
+      const int row = e / (D / 2), d = 2 * (e % (D / 2));
+      float mt = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kTokWarps; ++w) mt = fmaxf(mt, s_m[w][row]);
+      float lt = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll
+      for (int w = 0; w < kTokWarps; ++w) {
+        const float f = s_m[w][row] == -INFINITY ? 0.f : ex2(s_m[w][row] - mt);
+        lt = fmaf(s_l[w][row], f, lt);
+        if (f > 0.f) {
+          o0 = fmaf(s_o[w][row][d], f, o0);
+          o1 = fmaf(s_o[w][row][d + 1], f, o1);
+        }
+      }
+      if (whole) {
+        const float inv = lt > 0.f ? 1.f / lt : 0.f;
+        T* po = static_cast<T*>(a.out) + (static_cast<int64_t>(h) * a.G + row % a.G) * a.oh +
+                static_cast<int64_t>(q.t0 + row / a.G) * a.ot + d;
+        *reinterpret_cast<uint32_t*>(po) = pack_pair<T>(o0 * inv, o1 * inv);
+      } else {
+        *reinterpret_cast<float2*>(slot + row * D + d) = make_float2(o0, o1);
+        if (d == 0)
+          *reinterpret_cast<float2*>(slot + kTokenRows * D + 2 * row) = make_float2(mt, lt);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Joins the partial results of one (request, KV head), one CTA each; a warp per row at a time.
+template <typename T, int D>
+__global__ void __launch_bounds__(kTokThreads) token_combine_kernel(const PagedArgs a) {
+  __shared__ int s_sum[2][kTokWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv;
+  int before = 0, all = 0;
+  for (int i = tid; i < a.R; i += kTokThreads) {
+    const int n = token_chunks(a, load_request(a, i));
+    all += n;
+    if (i < r) before += n;
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  all = __reduce_add_sync(0xffffffffu, all);
+  if (lane == 0) {
+    s_sum[0][warp] = before;
+    s_sum[1][warp] = all;
+  }
+  __syncthreads();
+  before = all = 0;
+#pragma unroll
+  for (int w = 0; w < kTokWarps; ++w) {
+    before += s_sum[0][w];
+    all += s_sum[1][w];
+  }
+  const Request q = load_request(a, r);
+  const int nch = token_chunks(a, q);
+  if (nch == 0) return;
+  const int64_t span = token_span(static_cast<int64_t>(all) * a.Hkv, a.workers);
+  const int64_t u0 = static_cast<int64_t>(before) * a.Hkv + static_cast<int64_t>(h) * nch;
+  const int w0 = static_cast<int>(u0 / span), w1 = static_cast<int>((u0 + nch - 1) / span);
+  if (w0 == w1) return;  // one CTA had all of it and wrote the result
+  for (int row = warp; row < q.n * a.G; row += kTokWarps) {
+    float mt = -INFINITY;
+    for (int w = w0 + lane; w <= w1; w += 32)
+      mt = fmaxf(mt, token_slot(a, w, w == w0 ? 1 : 0, D)[kTokenRows * D + 2 * row]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+    float lt = 0.f, acc[D / 32] = {};
+#pragma unroll 4
+    for (int w = w0; w <= w1; ++w) {
+      const float* s = token_slot(a, w, w == w0 ? 1 : 0, D);
+      const float2 ml = *reinterpret_cast<const float2*>(s + kTokenRows * D + 2 * row);
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mt);
+      lt = fmaf(ml.y, f, lt);
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e) {
+        const float2 v = *reinterpret_cast<const float2*>(s + row * D + 64 * e + 2 * lane);
+        acc[2 * e] = fmaf(v.x, f, acc[2 * e]);
+        acc[2 * e + 1] = fmaf(v.y, f, acc[2 * e + 1]);
+      }
+    }
+    const float inv = lt > 0.f ? 1.f / lt : 0.f;
+    T* po = static_cast<T*>(a.out) + (static_cast<int64_t>(h) * a.G + row % a.G) * a.oh +
+            static_cast<int64_t>(q.t0 + row / a.G) * a.ot;
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e)
+      *reinterpret_cast<uint32_t*>(po + 64 * e + 2 * lane) = pack_pair<T>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  }
+}
+
+// ================================================================ tile kernel
+constexpr int kTileRows = 256;   // rows of a CTA: two 128-row tiles
+constexpr int kTileStages = 5;   // K/V stages of 128 rows
+constexpr int kTileInfo = 4;     // chunk records in flight
+constexpr int kTileThreads = 320;  // 8 softmax warps, one MMA warp, one TMA warp
+
+// A chunk's record: the key position of each of its eight 16-key granules (kAbsent where the
+// chunk holds none), the rows of it that hold keys, and the last position in it (kAbsent when
+// a granule is absent or a row of it lies behind the last key). rows == 0 ends the list.
+constexpr int kAbsent = 0x3fffffff;
+struct TileInfo {
+  int pos[8];
+  int rows, last;
+};
+
+template <int D>
+struct TileCfg {
+  static constexpr int TILE = 128 * D * 2;  // one operand tile
+  static constexpr int NATOM = D / 64;      // 128-byte column slices
+  static constexpr int MISC = 1024;
+  static constexpr int SMEM = (2 + kTileStages) * TILE + MISC + 1024;
+  // one CTA per SM: it takes all 512 TMEM columns
+  static constexpr int SMEM_LAUNCH = SMEM > 120 * 1024 ? SMEM : 120 * 1024;
+};
+
+enum {
+  TB_KV_FULL = 0,
+  TB_KV_EMPTY = TB_KV_FULL + kTileStages,
+  TB_INFO = TB_KV_EMPTY + kTileStages,
+  TB_Q = TB_INFO + kTileInfo,
+  TB_S,            // two: logits of a tile ready
+  TB_P = TB_S + 2,  // two: weights of a tile written
+  TB_O = TB_P + 2,  // two: output of a tile final
+  TB_DRAIN = TB_O + 2,
+  TB_COUNT
+};
+
+// Tile pair u of a KV head: its request and its index there (false past the last one). The
+// requests' pairs are counted by one warp, 32 requests at a time.
+__device__ __forceinline__ bool find_tile(const PagedArgs& a, int u, int lane, int* r_out, int* tile_out) {
+  int base = 0;
+  for (int r0 = 0; r0 < a.R; r0 += 32) {
+    const int r = r0 + lane;
+    int n = 0;
+    if (r < a.R) {
+      const int64_t rows = static_cast<int64_t>(load_request(a, r).n) * a.G;
+      n = rows > a.min_rows ? static_cast<int>((rows + kTileRows - 1) / kTileRows) : 0;
+    }
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, base + incl > u);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      *r_out = r0 + src;
+      *tile_out = u - base - __shfl_sync(0xffffffffu, incl - n, src);
+      return true;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return false;
+}
+
+__device__ __forceinline__ size_t tile_part_row(const PagedArgs& a, int u, int h, int split, int row) {
+  return ((static_cast<size_t>(u) * a.Hkv + h) * a.splits + split) * kTileRows + row;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    paged_tile_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const PagedArgs a) {
+  using Cfg = TileCfg<D>;
+  constexpr bool kF16 = std::is_same<T, __half>::value;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sQ = smem_u32(smem), sKV = sQ + 2 * Cfg::TILE;
+  uint8_t* misc = smem + (2 + kTileStages) * Cfg::TILE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(misc);
+  TileInfo* info = reinterpret_cast<TileInfo*>(misc + 8 * TB_COUNT);
+  int* ids = reinterpret_cast<int*>(info + kTileInfo);  // 8: page ids of the chunk being loaded
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ids + 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* never = reinterpret_cast<int*>(tmem_slot + 2);
+  int* where = reinterpret_cast<int*>(tmem_slot + 3);  // request, tile (or -1)
+  const uint32_t bar0 = smem_u32(bars);
+#define TBAR(i) (bar0 + 8u * static_cast<uint32_t>(i))
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int split = blockIdx.x % a.splits;
+  // causal tiles near the end of a request see the most keys: they start first
+  const int u = a.units_max - 1 - static_cast<int>(blockIdx.x / a.splits);
+  const int h = blockIdx.y;
+
+  if (warp == 0) {
+    int r = 0, tile = 0;
+    const bool found = find_tile(a, u, lane, &r, &tile);
+    if (lane == 0) {
+      where[0] = found ? r : -1;
+      where[1] = tile;
+    }
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+      for (int i = lane; i < a.R; i += 32) check_request(a, i);
+  } else if (warp == 1) {
+    if (lane == 0) {
+      for (int i = 0; i < TB_COUNT; ++i)
+        mbar_init(TBAR(i), i == TB_Q ? 256u : (i == TB_P || i == TB_P + 1 ? 128u : 1u));
+      *abort_flag = 0;
+      *never = 0;
+      fence_mbarrier_init();
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
+    }
+  }
+  __syncthreads();
+  const int r = where[0];
+  if (r < 0) return;  // no such tile: the same for the whole CTA
+  if (warp == 2) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  const Request q = load_request(a, r);
+  const int row0 = where[1] * kTileRows;
+  const int rows = min(kTileRows, q.n * a.G - row0);  // > 0
+  const bool two = rows > 128;
+  // keys that the CTA's last row sees, and this split's share of them in 128-key steps
+  const int last_tok = (row0 + rows - 1) / a.G;
+  const int key_end = a.causal ? min(q.len, q.ctx + last_tok + 1) : q.len;
+  const int steps = (key_end + 127) >> 7;
+  const int key_lo = static_cast<int>(static_cast<int64_t>(steps) * split / a.splits) << 7;
+  const int key_hi = min(key_end, static_cast<int>(static_cast<int64_t>(steps) * (split + 1) / a.splits) << 7);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // a warp waits as one: what follows a wait is warp-wide
+  auto wait_all = [&](uint32_t bar, uint32_t parity, int site) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, site));
+  };
+  if (warp == 9) {
+    // ------------------------------------------------ TMA warp: gathers chunks page by page
+    // A load takes lu = min(page, 128) rows; chunk = 128 / lu loads of kept pages, in order.
+    const int lu_shift = min(a.page_shift, 7), lu = 1 << lu_shift, per_chunk = 128 >> lu_shift;
+    const int32_t* trow = a.table + r * a.table_stride;
+    const uint8_t* mrow = a.mask ? a.mask + r * a.mr + h * a.mg : nullptr;
+    int cursor = key_lo >> lu_shift;
+    const int cursor_end = (key_hi + lu - 1) >> lu_shift;
+    uint32_t loads = 0;  // stages filled so far
+    bool ok = true;
+    for (int j = 0; ok; ++j) {
+      TileInfo* ti = info + j % kTileInfo;
+      int filled = 0, last_i = -1;
+      // the record is free: the stage of this chunk's keys was last used by the values of
+      // chunk j - 3, whose product waited for the softmax of that chunk
+      if (loads >= kTileStages)
+        ok = wait_all(TBAR(TB_KV_EMPTY + loads % kTileStages), ((loads / kTileStages) - 1) & 1, kPagedSite + 10);
+      if (!ok) break;
+      while (filled < per_chunk && cursor < cursor_end) {
+        const int i = cursor + lane;
+        int id = -1;
+        if (i < cursor_end) {
+          const int pg = static_cast<int>((static_cast<int64_t>(i) << lu_shift) >> a.page_shift);
+          if (!mrow || mrow[pg]) {
+            id = trow[pg];
+            if (id < 0 || id >= a.n_pages) {
+              report_device_error(kStatusBadLabel, kPagedSite + 1);
+              id = -1;
+            }
+          }
+        }
+        const unsigned kept = __ballot_sync(0xffffffffu, id >= 0);
+        const int rank = filled + __popc(kept & ((1u << lane) - 1u));
+        const bool take = id >= 0 && rank < per_chunk;
+        if (take) {
+          ids[rank] = id;
+          for (int gk = 0; gk < lu / 16; ++gk) ti->pos[rank * (lu / 16) + gk] = (i << lu_shift) + 16 * gk;
+        }
+        const unsigned taken = __ballot_sync(0xffffffffu, take);
+        const int n = __popc(taken);
+        filled += n;
+        if (n) last_i = cursor + 31 - __clz(taken);
+        cursor += filled == per_chunk ? (32 - __clz(taken)) : 32;
+      }
+      const int granules = filled * (lu / 16);
+      if (lane < 8 && lane >= granules) ti->pos[lane] = kAbsent;
+      // rows that hold keys: all of the loads but what lies behind the last key that a row of
+      // the CTA sees
+      int valid = filled * lu;
+      if (filled) valid -= max(0, ((last_i + 1) << lu_shift) - key_end);
+      if (lane == 0) {
+        ti->rows = valid;
+        ti->last = valid == 128 ? (last_i << lu_shift) + lu - 1 : kAbsent;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(TBAR(TB_INFO + j % kTileInfo));
+      if (filled == 0) break;
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t stage = loads % kTileStages;
+        if (kv == 1 && loads >= kTileStages) {
+          ok = wait_all(TBAR(TB_KV_EMPTY + stage), ((loads / kTileStages) - 1) & 1, kPagedSite + 11);
+          if (!ok) break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(TBAR(TB_KV_FULL + stage), filled * lu * D * 2);
+        __syncwarp();
+        if (lane < filled) {
+          const int i_row = a.page_shift > 7 ? ti->pos[0] & ((1 << a.page_shift) - 1) : 0;
+#pragma unroll
+          for (int cc = 0; cc < Cfg::NATOM; ++cc)
+            tma_load_4d(sKV + stage * Cfg::TILE + cc * 16384 + lane * lu * 128, kv ? &tmV : &tmK,
+                        TBAR(TB_KV_FULL + stage), cc * 64, i_row, h, ids[lane]);
+        }
+        __syncwarp();
+        ++loads;
+      }
+    }
+    // every copy has landed before the CTA may end
+    for (uint32_t i = loads > kTileStages ? loads - kTileStages : 0; i < loads; ++i)
+      mbar_wait(TBAR(TB_KV_FULL + i % kTileStages), (i / kTileStages) & 1, never, kPagedSite + 12);
+  } else if (warp == 8) {
+    // ------------------------------------------------ MMA warp
+    // Tile t's logits and, over them, its weights live in TMEM columns 128 t .., its output in
+    // 256 + 128 t ... While the softmax warps of one tile are at work, the other tile's
+    // products run: PV(t, j) then QK(t, j + 1), for t = 0 and 1 in turn.
+    auto commit = [&](uint32_t bar) {
+      if (elect_one()) tc_commit(bar);
+      __syncwarp();
+    };
+    constexpr uint32_t kIdQK = make_idesc16(kF16, 128, 128, false, false);
+    constexpr uint32_t kIdPV = make_idesc16(kF16, 128, D, false, true);
+    const uint64_t dQ = smem_desc(sQ, 16, 1024);
+    const uint64_t dKV = smem_desc(sKV, 16, 1024);
+    const uint64_t dV = smem_desc(sKV, 16384, 1024);
+    auto issue_qk = [&](int t, uint32_t stage) {
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t off = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+          mma_ss<false>(tmem + 128 * t, dQ + static_cast<uint64_t>((t * Cfg::TILE) >> 4) + off,
+                        dKV + static_cast<uint64_t>((stage * Cfg::TILE) >> 4) + off, kIdQK, kk > 0 ? 1u : 0u);
+        }
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](int t, uint32_t stage, bool first) {
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts<false>(tmem + 256 + 128 * t, tmem + 128 * t + kk * 8,
+                        dV + static_cast<uint64_t>((stage * Cfg::TILE + kk * 2048) >> 4), kIdPV,
+                        (!first || kk > 0) ? 1u : 0u);
+      }
+      __syncwarp();
+    };
+    bool ok = wait_all(TBAR(TB_Q), 0, kPagedSite + 20);
+    ok = ok && wait_all(TBAR(TB_INFO), 0, kPagedSite + 21);
+    int chunk_rows = ok ? info[0].rows : 0;
+    if (ok && chunk_rows > 0) {
+      ok = wait_all(TBAR(TB_KV_FULL), 0, kPagedSite + 22);
+      if (ok) {
+        tc_fence_after();
+        for (int t = 0; t < (two ? 2 : 1); ++t) {
+          issue_qk(t, 0);
+          commit(TBAR(TB_S + t));
+        }
+        commit(TBAR(TB_KV_EMPTY));
+      }
+    }
+    uint32_t load = 1;  // next stage to use: the values of chunk 0
+    for (int j = 0; ok && chunk_rows > 0; ++j) {
+      const uint32_t vst = load % kTileStages, vph = (load / kTileStages) & 1;
+      const uint32_t kst = (load + 1) % kTileStages, kph = ((load + 1) / kTileStages) & 1;
+      load += 2;
+      if (!(ok = wait_all(TBAR(TB_KV_FULL + vst), vph, kPagedSite + 23))) break;
+      if (chunk_rows < 128) {
+        // value rows without a key: zeros (what lies there may be anything, and 0 * NaN is NaN)
+        for (int i = chunk_rows * 8 + lane; i < 128 * 8; i += 32)
+#pragma unroll
+          for (int cc = 0; cc < Cfg::NATOM; ++cc)
+            *reinterpret_cast<uint4*>(smem + (2 + vst) * Cfg::TILE + cc * 16384 + i * 16) =
+                make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (!(ok = wait_all(TBAR(TB_INFO + (j + 1) % kTileInfo), ((j + 1) / kTileInfo) & 1, kPagedSite + 24))) break;
+      const int next_rows = info[(j + 1) % kTileInfo].rows;
+      for (int t = 0; ok && t < (two ? 2 : 1); ++t) {
+        if (!(ok = wait_all(TBAR(TB_P + t), j & 1, kPagedSite + 25))) break;
+        tc_fence_after();
+        issue_pv(t, vst, j == 0);
+        if (t == (two ? 1 : 0)) commit(TBAR(TB_KV_EMPTY + vst));
+        if (next_rows > 0) {
+          if (t == 0 && !(ok = wait_all(TBAR(TB_KV_FULL + kst), kph, kPagedSite + 26))) break;
+          tc_fence_after();
+          issue_qk(t, kst);
+          commit(TBAR(TB_S + t));
+        } else {
+          commit(TBAR(TB_O + t));
+        }
+      }
+      if (next_rows > 0) commit(TBAR(TB_KV_EMPTY + kst));
+      chunk_rows = next_rows;
+    }
+    // every product has completed before the CTA may end
+    commit(TBAR(TB_DRAIN));
+    mbar_wait(TBAR(TB_DRAIN), 0, never, kPagedSite + 27);
+  } else {
+    // ------------------------------------------------ softmax: one thread per row
+    const int t = warp >> 2, rr = tid & 127;
+    const int row = row0 + 128 * t + rr;
+    const bool live = 128 * t + rr < rows;
+    const int tok = row / a.G, hq = h * a.G + row % a.G;
+    // this row of Q into the swizzled tile (16-byte piece p of row rr at p ^ (rr & 7))
+    {
+      const T* src = static_cast<const T*>(a.q) + hq * a.qh + static_cast<int64_t>(q.t0 + tok) * a.qt;
+#pragma unroll
+      for (int p = 0; p < D / 8; ++p) {
+        const uint4 v = live ? *reinterpret_cast<const uint4*>(src + 8 * p) : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(smem + t * Cfg::TILE + (p >> 3) * 16384 + rr * 128 + (((p & 7) ^ (rr & 7)) << 4)) = v;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(TBAR(TB_Q));
+    }
+    const int lim = live ? (a.causal ? min(q.len - 1, q.ctx + tok) : q.len - 1) : -1;
+    // the smallest reach of the tile's rows (its first row's): chunks up to it need no mask
+    const int lim_tile = a.causal ? min(q.len - 1, q.ctx + (row0 + 128 * t) / a.G) : q.len - 1;
+    const uint32_t tS = tmem + 128 * t + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t tO = tS - 128 * t + 256 + 128 * t;
+    float m_run = -INFINITY, l_run = 0.f;
+    bool ok = t == 0 || two;
+    int nch = 0;
+#pragma unroll 1
+    for (int j = 0; ok; ++j) {
+      if (!(ok = wait_all(TBAR(TB_INFO + j % kTileInfo), (j / kTileInfo) & 1, kPagedSite + 30))) break;
+      const TileInfo* ti = info + j % kTileInfo;
+      if (ti->rows == 0) break;
+      const bool edge = ti->last > lim_tile;
+      if (!(ok = wait_all(TBAR(TB_S + t), j & 1, kPagedSite + 31))) break;
+      tc_fence_after();
+      ++nch;
+      float v[4][32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, v[i]);
+      tmem_wait_ld();
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int seen = lim - ti->pos[i];  // last visible column of the granule
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            if (c > seen) v[i >> 1][(i & 1) * 16 + c] = -INFINITY;
+        }
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx = max3(mx, max16(v[i]), max16(v[i] + 16));
+      mx *= a.scale_log2;
+      // Lazy rescaling: the running maximum moves when it is passed by more than 8 (base-2
+      // units), so the weights stay below 2^8 and the output is rarely touched. The logits'
+      // commit came after the previous product of this tile, so the output is at rest.
+      const bool need = mx > m_run + 8.f;
+      if (__any_sync(0xffffffffu, need)) {
+        float alpha = 1.f;
+        if (need) {
+          alpha = ex2(m_run - mx);
+          l_run *= alpha;
+          m_run = mx;
+        }
+        if (j > 0) {
+#pragma unroll 1
+          for (int p = 0; p < D / 32; ++p) {
+            float o[32];
+            tmem_ld32(tO + p * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] *= alpha;
+            tmem_st32(tO + p * 32, *reinterpret_cast<uint32_t(*)[32]>(o));
+          }
+        }
+      }
+      const float neg = m_run == -INFINITY ? 0.f : -m_run;
+      float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          float x0, x1;
+          fma2(x0, x1, v[i][2 * c], v[i][2 * c + 1], a.scale_log2, a.scale_log2, neg, neg);
+          x0 = ex2(x0);
+          x1 = ex2(x1);
+          if (c & 1) add2(sb0, sb1, sb0, sb1, x0, x1);
+          else add2(sa0, sa1, sa0, sa1, x0, x1);
+          w[c] = pack_pair<T>(x0, x1);
+        }
+        tmem_st16(tS + 16 * i, w);
+      }
+      l_run += (sa0 + sa1) + (sb0 + sb1);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(TBAR(TB_P + t));
+    }
+    if (ok && nch > 0) ok = wait_all(TBAR(TB_O + t), 0, kPagedSite + 32);
+    if (ok && (t == 0 || two)) {
+      tc_fence_after();
+      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      T* po = static_cast<T*>(a.out) + hq * a.oh + static_cast<int64_t>(q.t0 + tok) * a.ot;
+      const size_t prow = a.splits > 1 ? tile_part_row(a, u, h, split, 128 * t + rr) : 0;
+      const size_t all_rows = static_cast<size_t>(a.units_max) * a.Hkv * a.splits * kTileRows;
+#pragma unroll 1
+      for (int p = 0; p < D / 32; ++p) {
+        float o[32];
+        if (nch > 0) {
+          tmem_ld32(tO + p * 32, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = 0.f;
+        }
+        if (live && a.splits > 1) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<float4*>(a.part + prow * D + p * 32 + 4 * c) =
+                make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+        } else if (live) {
+          uint32_t w[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            w[c] = l_run > 0.f ? pack_pair<T>(o[2 * c] * inv, o[2 * c + 1] * inv) : 0u;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4*>(po + p * 32 + 8 * c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        }
+        __syncwarp();
+      }
+      if (live && a.splits > 1)
+        *reinterpret_cast<float2*>(a.part + all_rows * D + prow * 2) = make_float2(m_run, l_run);
+    }
+  }
+#undef TBAR
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the key splits of a tile pair: grid (units, Hkv, 8 row groups), a warp per row.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) tile_combine_kernel(const PagedArgs a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int r = 0, tile = 0;
+  const int u = blockIdx.x, h = blockIdx.y;
+  if (!find_tile(a, u, lane, &r, &tile)) return;
+  const Request q = load_request(a, r);
+  const int rows = min(kTileRows, q.n * a.G - tile * kTileRows);
+  const float* ml = a.part + static_cast<size_t>(a.units_max) * a.Hkv * a.splits * kTileRows * D;
+  for (int rr = blockIdx.z * 8 + warp; rr < rows; rr += 64) {
+    float mt = -INFINITY;
+    for (int s = 0; s < a.splits; ++s) mt = fmaxf(mt, ml[2 * tile_part_row(a, u, h, s, rr)]);
+    float lt = 0.f, acc[D / 32] = {};
+    for (int s = 0; s < a.splits; ++s) {
+      const size_t prow = tile_part_row(a, u, h, s, rr);
+      const float2 x = *reinterpret_cast<const float2*>(ml + 2 * prow);
+      if (x.y <= 0.f) continue;  // a split that saw no key of this row
+      const float f = ex2(x.x - mt);
+      lt = fmaf(x.y, f, lt);
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e) {
+        const float2 o = *reinterpret_cast<const float2*>(a.part + prow * D + 64 * e + 2 * lane);
+        acc[2 * e] = fmaf(o.x, f, acc[2 * e]);
+        acc[2 * e + 1] = fmaf(o.y, f, acc[2 * e + 1]);
+      }
+    }
+    const float inv = lt > 0.f ? 1.f / lt : 0.f;
+    const int row = tile * kTileRows + rr;
+    T* po = static_cast<T*>(a.out) + (static_cast<int64_t>(h) * a.G + row % a.G) * a.oh +
+            static_cast<int64_t>(q.t0 + row / a.G) * a.ot;
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e)
+      *reinterpret_cast<uint32_t*>(po + 64 * e + 2 * lane) = pack_pair<T>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  }
+}
+
+// ================================================================ host side
+struct PagedPlan {
+  bool token, tile;  // which kernels run
+  int min_rows;      // rows up to which a request is the token kernel's
+  int workers, one_each;
+  int units_max, splits;
+  size_t bytes;
+  size_t tile_off;
+};
+
+constexpr int kTokCtas = 148 * 3;
+
+PagedPlan paged_plan(int R, int T, int Hq, int Hkv, int D, int max_new, int width, int page) {
+  PagedPlan p{};
+  const int G = Hq / Hkv;
+  const int64_t most = static_cast<int64_t>(std::min(max_new, T)) * G;
+  p.token = most <= kTokenRows || R > 1;
+  p.tile = most > kTokenRows;
+  p.min_rows = p.token ? kTokenRows : 0;
+  const int64_t keys = static_cast<int64_t>(width) * page;
+  p.one_each = keys <= kTokMinSpan * kTokChunk;
+  p.workers = p.one_each ? R * Hkv : kTokCtas;
+  size_t b = 0;
+  if (p.token && !p.one_each)
+    b = align_up(static_cast<size_t>(p.workers) * 2 * kTokenRows * (D + 2) * sizeof(float), 256);
+  p.tile_off = b;
+  p.splits = 1;
+  if (p.tile) {
+    // a request's tiles: at most its rows / 256 rounded up; the sum over requests is at most
+    p.units_max = static_cast<int>(static_cast<int64_t>(T) * G / kTileRows + std::min(R, T));
+    const int64_t ctas = static_cast<int64_t>(p.units_max) * Hkv;
+    const int64_t most_splits = std::max<int64_t>(1, std::min<int64_t>(16, keys / 1024));
+    if (ctas < 148) p.splits = static_cast<int>(std::min<int64_t>(most_splits, 148 / ctas));
+    if (p.splits > 1)
+      b += align_up(static_cast<size_t>(ctas) * p.splits * kTileRows * (D + 2) * sizeof(float), 256);
+  }
+  p.bytes = std::max<size_t>(b, 256);
+  return p;
+}
+
+int check_paged_sizes(const bsa_paged_cache& c, int R, int T, int Hq, int max_new, int width) {
+  const int st = check_paged_cache(c);
+  if (st != BSA_OK) return st;
+  if (R < 0 || T < 0 || Hq <= 0 || max_new < 0 || width < 0) return fail(BSA_ERR_INVALID_ARG, "bad size");
+  if (Hq % c.Hkv) return fail(BSA_ERR_INVALID_ARG, "Hq (%d) not a multiple of Hkv (%d)", Hq, c.Hkv);
+  if (R > kPagedMaxR) return fail(BSA_ERR_UNSUPPORTED, "%d requests, at most %d", R, kPagedMaxR);
+  if (c.Hkv > 4096 || Hq > 16384) return fail(BSA_ERR_UNSUPPORTED, "too many heads");
+  if (static_cast<int64_t>(T) * Hq > INT32_MAX / 2) return fail(BSA_ERR_UNSUPPORTED, "T*Hq exceeds 2^30");
+  if (static_cast<int64_t>(width) * c.page > (1 << 28))
+    return fail(BSA_ERR_UNSUPPORTED, "a request of more than 2^28 keys");
+  if (static_cast<int64_t>(width) * c.page * R > (int64_t(1) << 36))
+    return fail(BSA_ERR_UNSUPPORTED, "block table of more than 2^36 keys");
+  return BSA_OK;
+}
+
+template <typename T, int D>
+int launch_paged(PagedArgs a, const PagedPlan& p, const bsa_paged_cache& c, char* ws, cudaStream_t st) {
+  if (p.token) {
+    PagedArgs t = a;
+    t.part = reinterpret_cast<float*>(ws);
+    t.workers = p.workers;
+    t.one_each = p.one_each;
+    const int smem = p.one_each ? 0 : (a.R + 1) * static_cast<int>(sizeof(int32_t));
+    const int64_t most = static_cast<int64_t>(std::min(a.max_new, a.T)) * a.G;
+    t.tok_rows = most <= 8 ? 8 : kTokenRows;
+    auto kern = most <= 8 ? paged_token_kernel<T, D, 1> : paged_token_kernel<T, D, 2>;
+    if (smem > 8192) {  // with the static part past the 48 KB that need no opt-in
+      const int e = check_cuda(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
+                               "cudaFuncSetAttribute(paged_token_kernel)");
+      if (e != BSA_OK) return e;
+    }
+    kern<<<p.workers, kTokThreads, smem, st>>>(t);
+    count_launch();
+    if (!p.one_each) {
+      token_combine_kernel<T, D><<<a.R * a.Hkv, kTokThreads, 0, st>>>(t);
+      count_launch();
+    }
+    const int e = check_cuda(cudaGetLastError(), "paged_token_kernel");
+    if (e != BSA_OK) return e;
+  }
+  if (p.tile) {
+    PagedArgs t = a;
+    t.part = reinterpret_cast<float*>(ws + p.tile_off);
+    t.min_rows = p.min_rows;
+    t.splits = p.splits;
+    t.units_max = p.units_max;
+    CUtensorMap mk, mv;
+    const CUtensorMapDataType dt = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(c.page),
+                              static_cast<uint64_t>(c.Hkv), static_cast<uint64_t>(c.n_pages)};
+    const uint32_t box[4] = {64, static_cast<uint32_t>(std::min(c.page, 128)), 1, 1};
+    const uint64_t ks[3] = {static_cast<uint64_t>(c.k_row_stride) * 2, static_cast<uint64_t>(c.k_head_stride) * 2,
+                            static_cast<uint64_t>(c.k_page_stride) * 2};
+    const uint64_t vs[3] = {static_cast<uint64_t>(c.v_row_stride) * 2, static_cast<uint64_t>(c.v_head_stride) * 2,
+                            static_cast<uint64_t>(c.v_page_stride) * 2};
+    int e = make_tmap_4d(&mk, c.k, dt, 2, dims, ks, box);
+    if (e == BSA_OK) e = make_tmap_4d(&mv, c.v, dt, 2, dims, vs, box);
+    if (e != BSA_OK) return e;
+    auto kern = paged_tile_kernel<T, D>;
+    e = check_cuda(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        TileCfg<D>::SMEM_LAUNCH), "cudaFuncSetAttribute(paged_tile_kernel)");
+    if (e != BSA_OK) return e;
+    kern<<<dim3(p.units_max * p.splits, a.Hkv), kTileThreads, TileCfg<D>::SMEM_LAUNCH, st>>>(mk, mv, t);
+    count_launch();
+    if (p.splits > 1) {
+      tile_combine_kernel<T, D><<<dim3(p.units_max, a.Hkv, 8), 256, 0, st>>>(t);
+      count_launch();
+    }
+    e = check_cuda(cudaGetLastError(), "paged_tile_kernel");
+    if (e != BSA_OK) return e;
+  }
+  return BSA_OK;
+}
+
+}  // namespace
+}  // namespace bsa
+
+extern "C" {
+
+size_t bsa_paged_attention_workspace_bytes(bsa_paged_cache cache, int R, int T, int Hq, int max_new,
+                                           int width) {
+  if (bsa::check_paged_sizes(cache, R, T, Hq, max_new, width) != BSA_OK) return 0;
+  return bsa::paged_plan(R, T, Hq, cache.Hkv, cache.D, max_new, width, cache.page).bytes;
+}
+
+int bsa_paged_chunk_attention(bsa_heads q, bsa_paged_cache cache, const int32_t* block_table,
+                              int width, int64_t table_stride, const int32_t* cu_new,
+                              const int32_t* context_lens, int R, int T, int Hq, int max_new,
+                              const uint8_t* page_mask, int64_t mask_r_stride,
+                              int64_t mask_g_stride, float scale, int causal, bsa_heads out,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace bsa;
+  int st = check_paged_sizes(cache, R, T, Hq, max_new, width);
+  if (st != BSA_OK) return st;
+  if (R == 0 || T == 0 || max_new == 0 || width == 0) return BSA_OK;
+  if (!block_table || !cu_new || !context_lens || !q.ptr || !out.ptr)
+    return fail(BSA_ERR_INVALID_ARG, "null pointer");
+  if (reinterpret_cast<uintptr_t>(q.ptr) % 16 || reinterpret_cast<uintptr_t>(out.ptr) % 16 ||
+      q.stride_h % 8 || q.stride_s % 8 || out.stride_h % 8 || out.stride_s % 8)
+    return fail(BSA_ERR_INVALID_ARG, "q or out: pointer or strides not multiples of 16 bytes");
+  if (table_stride < 0 || mask_r_stride < 0 || mask_g_stride < 0)
+    return fail(BSA_ERR_INVALID_ARG, "negative stride");
+  const PagedPlan p = paged_plan(R, T, Hq, cache.Hkv, cache.D, max_new, width, cache.page);
+  if (!workspace || workspace_bytes < p.bytes)
+    return fail(BSA_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, p.bytes);
+  if (reinterpret_cast<uintptr_t>(workspace) % 256)
+    return fail(BSA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  PagedArgs a{};
+  a.q = q.ptr;
+  a.qh = q.stride_h;
+  a.qt = q.stride_s;
+  a.kc = cache.k;
+  a.vc = cache.v;
+  a.kp = cache.k_page_stride;
+  a.kh = cache.k_head_stride;
+  a.kr = cache.k_row_stride;
+  a.vp = cache.v_page_stride;
+  a.vh = cache.v_head_stride;
+  a.vr = cache.v_row_stride;
+  a.n_pages = cache.n_pages;
+  a.page_shift = __builtin_ctz(cache.page);
+  a.Hkv = cache.Hkv;
+  a.G = Hq / cache.Hkv;
+  a.T = T;
+  a.R = R;
+  a.table = block_table;
+  a.width = width;
+  a.table_stride = table_stride;
+  a.cu = cu_new;
+  a.ctx = context_lens;
+  a.mask = page_mask;
+  a.mr = mask_r_stride;
+  a.mg = mask_g_stride;
+  a.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(cache.D))) * 1.4426950408889634f;
+  a.causal = causal ? 1 : 0;
+  a.out = out.ptr;
+  a.oh = out.stride_h;
+  a.ot = out.stride_s;
+  a.max_new = max_new;
+  char* ws = static_cast<char*>(workspace);
+  cudaStream_t cs = as_stream(stream);
+  if (cache.dtype == BSA_F16)
+    return cache.D == 64 ? launch_paged<__half, 64>(a, p, cache, ws, cs)
+                         : launch_paged<__half, 128>(a, p, cache, ws, cs);
+  return cache.D == 64 ? launch_paged<__nv_bfloat16, 64>(a, p, cache, ws, cs)
+                       : launch_paged<__nv_bfloat16, 128>(a, p, cache, ws, cs);
+}
+
+}  // extern "C"

@@ -129,6 +129,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar,
+                                            int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
 // Four rows of a 2-D tensor map whose box is one row high, at columns [x, x + box) of
 // rows r0..r3, written to dst as four consecutive box rows (tile::gather4). A row
 // outside the tensor reads the fill value (zeros).
@@ -308,6 +317,13 @@ __host__ __device__ constexpr uint32_t make_idesc(bool tf32, int M, int N, bool 
          | ((tf32 ? 2u : 1u) << 10)                // B format
          | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// The same for kind::f16 with fp16 (f16 = true) or bf16 operands.
+__host__ __device__ constexpr uint32_t make_idesc16(bool f16, int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+         ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
 }
 
 // Packed fp32 pair arithmetic (sm_100a f32x2): d = a*b + c and d = a + b, elementwise.

@@ -50,7 +50,8 @@ enum {
   BSA_ERR_WORKSPACE = -5      /* workspace missing or too small */
 };
 
-enum { BSA_BF16 = 0, BSA_F32 = 1 };
+/* Element types. BSA_F16 is taken by the per-head norm and paged-cache entry points only. */
+enum { BSA_BF16 = 0, BSA_F32 = 1, BSA_F16 = 2 };
 
 /* Flags of bsa_centroid_compensated_attention_ex. */
 enum { BSA_REUSE_PLAN = 1 };
@@ -466,6 +467,164 @@ int bsa_mask_cache_layer_gate(void* state, uint8_t* refresh, int n_refresh_layer
                               int n_heads_layer, float gate_lo, float gate_hi, void* stream);
 /* Forgets anchors and masks: the next should_refresh refreshes every head. */
 int bsa_mask_cache_reset(void* state, void* stream);
+
+/*
+ * Per-head norms of queries and keys with the position rotation in the same pass (no
+ * counterpart on the pages: the step a video DiT layer runs on its projections before
+ * every attention, scoring and routing call of this library; it also lays the heads out
+ * the way those calls read them).
+ *
+ * A bsa_heads is a (B, H, S, D) tensor with element (b, h, s, d) at
+ * b*stride_b + h*stride_h + s*stride_s + d: heads-major, token-major and slices of a
+ * fused projection alike. Pointers must be 16-byte aligned and strides multiples of 16
+ * bytes (0 broadcasts an input); else BSA_ERR_INVALID_ARG.
+ */
+typedef struct {
+  void* ptr;
+  int64_t stride_b, stride_h, stride_s; /* elements */
+} bsa_heads;
+
+/*
+ * qk_norm_rotation. For every row x (D values) of q and k, with the weight w of its side
+ * and the cosines and sines of its token's position p:
+ *   y = x * (mean_d x_d^2 + eps)^(-1/2) * w
+ *   (out_a, out_b) = (y_a cos[p,i] - y_b sin[p,i], y_a sin[p,i] + y_b cos[p,i])
+ * over the pairs (a, b) = (2i, 2i+1) (interleaved != 0) or (i, i + D/2), i < D/2. All of
+ * it in fp32, rounded once to the output type.
+ *   q, k        : inputs (B, Hq, S, D) and (B, Hkv, S, D); shape.Sq == shape.Sk == S,
+ *                 shape.dtype BSA_BF16, BSA_F16 or BSA_F32, D in {64, 128}.
+ *   q_weight, k_weight : device (D), float32 (weight_f32 != 0) or of shape.dtype.
+ *   cos, sin    : device float32 (n_pos, D/2), 16-byte aligned.
+ *   positions   : device int32, token (b, s) at b*pos_b_stride + s; NULL = s. A row whose
+ *                 position is -1 is padding and its output is left as it was; so is one
+ *                 outside [0, n_pos), which also records BSA_ERR_INVALID_ARG in the device
+ *                 status.
+ *   q_out, k_out: outputs; an output may be its own input (same pointer and strides), but
+ *                 may not overlap it in another way.
+ * S == 0 or B == 0 returns BSA_OK without a launch. No workspace.
+ */
+int bsa_qk_norm_rotation(bsa_heads q, bsa_heads k, bsa_shape shape, const void* q_weight,
+                         const void* k_weight, int weight_f32, const float* cos, const float* sin,
+                         int n_pos, const int32_t* positions, int64_t pos_b_stride, float eps,
+                         int interleaved, bsa_heads q_out, bsa_heads k_out, void* stream);
+
+/*
+ * qk_norm_rotation_backward: gradients of the call above. With z = R(p)^T dout (the rotation
+ * by the negative angle), r = (mean x^2 + eps)^(-1/2) and g = z * w,
+ *   dx = r (g - x r^2 mean_d(g x)),   dw_d = sum over batch, head and token of z_d x_d r.
+ * The input gradients are computed in fp32 and rounded once; the weight gradients are
+ * fp32 and their sums run in a fixed order (the same call gives the same bits).
+ *   dq_out, dk_out : gradients of q_out, k_out (type of shape.dtype; any strides).
+ *   dq, dk         : written. Rows of skipped positions (see above) get zeros.
+ *   dq_weight, dk_weight : device float32 (D), written.
+ *   workspace      : >= bsa_qk_norm_rotation_workspace_bytes(shape), 256-byte aligned.
+ */
+size_t bsa_qk_norm_rotation_workspace_bytes(bsa_shape shape);
+int bsa_qk_norm_rotation_backward(bsa_heads dq_out, bsa_heads dk_out, bsa_heads q, bsa_heads k,
+                                  bsa_shape shape, const void* q_weight, const void* k_weight,
+                                  int weight_f32, const float* cos, const float* sin, int n_pos,
+                                  const int32_t* positions, int64_t pos_b_stride, float eps,
+                                  int interleaved, bsa_heads dq, bsa_heads dk, float* dq_weight,
+                                  float* dk_weight, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/*
+ * Paged key/value cache, for video that is generated chunk by chunk: a pool of n_pages
+ * pages of `page` tokens, K and V apart, element (page i, head g, row j, d) at
+ * i*page_stride + g*head_stride + j*row_stride + d of each. A request's tokens live in
+ * the pages its block-table row names, in order.
+ *   page  : 16, 32, 64, 128 or 256; n_pages * page < 2^31.
+ *   dtype : BSA_BF16 or BSA_F16. D in {64, 128}. Pointers 16-byte aligned, strides
+ *           multiples of 16 bytes.
+ */
+typedef struct {
+  void *k, *v;
+  int n_pages, page, Hkv, D;
+  int dtype;
+  int64_t k_page_stride, k_head_stride, k_row_stride; /* elements */
+  int64_t v_page_stride, v_head_stride, v_row_stride;
+} bsa_paged_cache;
+
+/*
+ * paged_block_tables: block tables and slot maps of a step, from the requests' lengths.
+ * Request r holds context_lens[r] tokens (in ceil(context/page) pages, named by its row of
+ * block_table) and takes new_lens[r] more. New pages come from free_pages in order, request
+ * by request:
+ *   have_r  = ceil(context_r / page),  need_r = ceil((context_r + new_r) / page) - have_r
+ *   block_table[r][have_r + i] = free_pages[sum of need over earlier requests + i]
+ *   slot of a token at position p of request r = block_table[r][p / page]*page + p % page
+ *   context_lens, new_lens : device int32 (R), R <= 4096.
+ *   block_table : device int32, row r at r*table_stride, `width` entries; updated.
+ *   free_pages  : device int32 (n_free).
+ *   slots, positions : device int32 (T), written: the requests' new tokens one after
+ *                 another; entries behind the last request's are -1.
+ *   cu_new      : device int32 (R + 1), written: running sums of new_lens (capped at T).
+ *   taken       : device int32, written: the pages that were needed. More than n_free means
+ *                 that the pool ran out: the pages past its end are -1 in block_table, and
+ *                 their tokens have slot -1.
+ * Negative lengths count as 0, a request past `width` pages gets slot -1 for the tokens
+ * there, and a page outside [0, n_pages) gives slot -1; these, and more than T new tokens,
+ * record BSA_ERR_INVALID_ARG in the device status. The same call may be repeated (it writes
+ * the same entries). R == 0 or T == 0 writes cu_new, taken and the padding. No workspace.
+ */
+int bsa_paged_block_tables(const int32_t* context_lens, const int32_t* new_lens, int R,
+                           int32_t* block_table, int width, int64_t table_stride,
+                           const int32_t* free_pages, int n_free, int T, int page, int n_pages,
+                           int32_t* slots, int32_t* positions, int32_t* cu_new, int32_t* taken,
+                           void* stream);
+
+/*
+ * paged_qk_norm_append: qk_norm_rotation of T packed tokens with the keys written straight
+ * into the cache, and the values copied beside them. Token t's key and value go to page
+ * slots[t] / page, row slots[t] % page. Type and D are the cache's; q is (Hq, T, D), k and v
+ * (Hkv, T, D) (stride_b is not read).
+ *   positions : device int32 (T), as above: -1 skips the token (nothing is written).
+ *   slots     : device int32 (T); -1 leaves the cache as it was and writes q_out alone, a
+ *               slot outside [0, n_pages*page) does the same and records
+ *               BSA_ERR_INVALID_ARG. Slots of one call must differ: which token's row a
+ *               slot named twice holds is not defined.
+ */
+int bsa_paged_qk_norm_append(bsa_heads q, bsa_heads k, bsa_heads v, int T, int Hq,
+                             const void* q_weight, const void* k_weight, int weight_f32,
+                             const float* cos, const float* sin, int n_pos,
+                             const int32_t* positions, const int32_t* slots, float eps,
+                             int interleaved, bsa_heads q_out, bsa_paged_cache cache,
+                             void* stream);
+
+/*
+ * paged_chunk_attention: attention of every request's new tokens over its cached ones and
+ * themselves (appended before), block-sparse at page granularity when a page mask is given
+ * ([SPR]: K/V partitions and routes are shared by a KV head's query heads). Token i of
+ * request r (position context_r + i) of query head h attends, with KV head
+ * g = h / (Hq / Hkv), to the keys j of request r with
+ *   j < context_r + new_r,  j <= context_r + i when causal,  page_mask[r][g][j / page] != 0:
+ *   out = sum_j softmax_j(scale q . k_j) v_j        (a row that no key is left for gets 0)
+ *   q         : device (Hq, T, D) of the cache's type, packed (stride_b not read).
+ *   block_table : device int32, row r at r*table_stride, `width` entries. A page outside
+ *               [0, n_pages) counts as masked and records BSA_ERR_INVALID_ARG.
+ *   cu_new    : device int32 (R + 1): request r's tokens are [cu_new[r], cu_new[r+1]).
+ *               Rows from cu_new[R] on are left as they were. R <= 4096.
+ *   context_lens : device int32 (R).
+ *   max_new   : host bound of the requests' new tokens (1 for a step of single tokens); a
+ *               request with more records BSA_ERR_INVALID_ARG and its rows may be left as
+ *               they were.
+ *   page_mask : device uint8, element (r, g, page index in the request) at
+ *               r*mask_r_stride + g*mask_g_stride + index; NULL keeps every page.
+ *   scale     : <= 0 selects 1/sqrt(D). out: (Hq, T, D) of the cache's type, any strides.
+ *   workspace : >= bsa_paged_attention_workspace_bytes(cache, R, T, Hq, max_new, width).
+ * Rows of the cache behind a request's last token, and masked pages, are never read into a
+ * result (they may hold NaN). A NaN or infinity in a value row that some token of a causal
+ * chunk sees may also reach tokens of the chunk that do not see it (their weight 0 times it). Hq a multiple of Hkv. fp32 logits, sums and accumulators; the
+ * weights are rounded to the cache's type before the second product.
+ */
+size_t bsa_paged_attention_workspace_bytes(bsa_paged_cache cache, int R, int T, int Hq,
+                                           int max_new, int width);
+int bsa_paged_chunk_attention(bsa_heads q, bsa_paged_cache cache, const int32_t* block_table,
+                              int width, int64_t table_stride, const int32_t* cu_new,
+                              const int32_t* context_lens, int R, int T, int Hq, int max_new,
+                              const uint8_t* page_mask, int64_t mask_r_stride,
+                              int64_t mask_g_stride, float scale, int causal, bsa_heads out,
+                              void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
