@@ -14,6 +14,7 @@ from .ops import (  # noqa: F401
     centroid_compensated_attention,
     device_status,
     error_aware_block_mask,
+    paged_attention_workspace_bytes,
     paged_block_tables,
     paged_chunk_attention,
     paged_qk_norm_append,

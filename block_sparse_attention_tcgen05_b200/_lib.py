@@ -132,6 +132,24 @@ def load():
     return _lib
 
 
+_native = None
+
+
+def native():
+    """The native marshalling module (built in-tree by ``build.py`` beside libbsa.so). Raises
+    if it is missing."""
+    global _native
+    if _native is None:
+        import importlib
+        load()
+        try:
+            _native = importlib.import_module("block_sparse_attention_tcgen05_b200._native")
+        except ImportError as e:
+            raise RuntimeError("_native.so cannot be loaded; build it with "
+                               "`python -m block_sparse_attention_tcgen05_b200.build`") from e
+    return _native
+
+
 def detail():
     buf = ctypes.create_string_buffer(512)
     load().bsa_last_error_detail(buf, 512)

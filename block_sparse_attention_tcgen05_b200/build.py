@@ -1,13 +1,17 @@
-"""Builds libbsa.so (the C-ABI library) in-tree with nvcc for sm_100a."""
+"""Builds libbsa.so (the C-ABI library, nvcc for sm_100a) and _native.so (the native
+marshalling of the calls that run down to single tokens, g++ against torch) in-tree."""
 
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libbsa.so")
 SRC = os.path.join(HERE, "csrc", "libbsa.cu")
+NATIVE = os.path.join(HERE, "_native.so")
+NATIVE_SRC = os.path.join(HERE, "csrc", "binding.cpp")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [
@@ -33,20 +37,44 @@ def up_to_date():
     return all(os.path.getmtime(s) <= t for s in sources())
 
 
-def build(force=False, verbose=False, extra=()):
-    """Compile libbsa.so unless it is newer than every source. Returns its path."""
-    if not force and up_to_date():
-        return LIB
-    cmd = [NVCC, *FLAGS, *extra, SRC, "-o", LIB + ".tmp"]
+def _native_command(out):
+    import torch
+    t = os.path.dirname(torch.__file__)
+    inc = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[x for i in inc for x in ("-isystem", i)], NATIVE_SRC, "-o", out,
+            "-L", HERE, "-l:libbsa.so", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(t, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
+def _compile(cmd, out, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("nvcc failed building libbsa.so")
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed building {os.path.basename(out)}")
     if verbose and (r.stdout or r.stderr):
         sys.stderr.write(r.stdout + r.stderr)
-    os.replace(LIB + ".tmp", LIB)
+    os.replace(out + ".tmp", out)
+
+
+def build_native(force=False, verbose=False):
+    """Compile _native.so unless it is newer than its sources. Returns its path."""
+    srcs = (NATIVE_SRC, os.path.join(ROOT, "include", "bsa.h"))
+    if force or not os.path.exists(NATIVE) or any(os.path.getmtime(s) > os.path.getmtime(NATIVE) for s in srcs):
+        _compile(_native_command(NATIVE + ".tmp"), NATIVE, verbose)
+    return NATIVE
+
+
+def build(force=False, verbose=False, extra=()):
+    """Compile libbsa.so and _native.so unless they are newer than their sources. Returns the
+    path of libbsa.so."""
+    if force or not up_to_date():
+        _compile([NVCC, *FLAGS, *extra, SRC, "-o", LIB + ".tmp"], LIB, verbose)
+    build_native(force, verbose)
     return LIB
 
 

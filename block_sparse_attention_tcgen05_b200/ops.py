@@ -14,6 +14,7 @@ from . import _lib
 from ._lib import BSA_BF16, BSA_F32, Shape, call
 
 _DT = {torch.bfloat16: BSA_BF16, torch.float32: BSA_F32}
+_DT_PAGED = {torch.bfloat16: BSA_BF16, torch.float16: _lib.BSA_F16}
 
 
 def _stream(dev):
@@ -473,82 +474,8 @@ class MaskCache:
         _call_on(self.state.device, "bsa_mask_cache_reset", _ptr(self.state), _stream(self.state.device))
 
 
-# Element types of the per-head norm and the paged cache.
-_DT_HEADS = {torch.bfloat16: _lib.BSA_BF16, torch.float16: _lib.BSA_F16, torch.float32: _lib.BSA_F32}
-_DT_PAGED = {torch.bfloat16: _lib.BSA_BF16, torch.float16: _lib.BSA_F16}
-
-
-def _same_device(*ts):
-    """As ``_need_cuda`` for calls that take strided tensors."""
-    present = [t for t in ts if t is not None]
-    devs = {t.device for t in present}
-    if len(devs) > 1:
-        raise ValueError(f"all tensors of one call must be on the same device, got "
-                         f"{sorted(str(d) for d in devs)}")
-    for t in present:
-        if not t.is_cuda:
-            raise ValueError("libbsa operates on CUDA tensors only")
-
-
-def _heads(t, name, written=False):
-    """bsa_heads of a (B,H,S,D) or packed (H,T,D) tensor: any strides that are multiples of
-    16 bytes, D contiguous. The stride of a dimension of size 1 is never used and passed as 0;
-    an output may not be broadcast."""
-    unit = 16 // t.element_size()
-    if t.numel() and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    st = [s if n > 1 else 0 for s, n in zip(t.stride(), t.shape)]
-    st = ([0] if t.dim() == 3 else []) + st[:-1]
-    if t.numel() and (t.data_ptr() % 16 or any(s % unit for s in st)):
-        raise ValueError(f"{name}: pointer and strides must be multiples of 16 bytes")
-    if written and any(s == 0 and n > 1 for s, n in zip(t.stride(), t.shape)):
-        raise ValueError(f"{name}: an output may not be broadcast")
-    return _lib.Heads(t.data_ptr(), *st)
-
-
-def _expect_table(cos, sin, D):
-    _expect(cos, "cos", (torch.float32,), (2,))
-    if cos.shape[1] != D // 2:
-        raise ValueError(f"cos: shape {tuple(cos.shape)}, expected (positions, {D // 2})")
-    _expect(sin, "sin", (torch.float32,), (2,), tuple(cos.shape))
-    for t, name in ((cos, "cos"), (sin, "sin")):
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: must be contiguous")
-        if t.numel() and t.data_ptr() % 16:
-            raise ValueError(f"{name}: pointer must be a multiple of 16 bytes")
-
-
-def _expect_weights(q_weight, k_weight, dtype, D):
-    """1 if the weights are fp32, 0 if of the heads' type."""
-    _expect(q_weight, "q_weight", (torch.float32, dtype), (1,), (D,))
-    _expect(k_weight, "k_weight", (q_weight.dtype,), (1,), (D,))
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: must be contiguous")
-    return 1 if q_weight.dtype == torch.float32 else 0
-
-
-def _expect_positions(positions, B, S):
-    """int32 (S,) or (B, S) -> batch stride."""
-    if positions is None:
-        return 0
-    _expect(positions, "positions", (torch.int32,), (1, 2))
-    if tuple(positions.shape) not in ((S,), (B, S)):
-        raise ValueError(f"positions: shape {tuple(positions.shape)}, expected ({S},) or ({B}, {S})")
-    if not positions.is_contiguous():
-        raise ValueError("positions: must be contiguous")
-    return S if positions.dim() == 2 else 0
-
-
-def _norm_shape(q, k, cos, positions):
-    _expect(q, "q", tuple(_DT_HEADS), (4,))
-    _expect(k, "k", (q.dtype,), (4,))
-    B, Hq, S, D = q.shape
-    if k.shape[0] != B or k.shape[2] != S or k.shape[3] != D or k.shape[1] <= 0:
-        raise ValueError(f"k: shape {tuple(k.shape)} does not fit q {tuple(q.shape)}")
-    if positions is None and cos.shape[0] < S:
-        raise ValueError(f"cos: {cos.shape[0]} positions for {S} tokens")
-    return Shape(B, Hq, k.shape[1], S, S, D, _DT_HEADS[q.dtype])
+# The calls below run down to single tokens, so their marshalling (checks, allocations, the
+# library call) is native: csrc/binding.cpp.
 
 
 def qk_norm_rotation(q, k, q_weight, k_weight, cos, sin, positions=None, eps=1e-6,
@@ -561,34 +488,8 @@ def qk_norm_rotation(q, k, q_weight, k_weight, cos, sin, positions=None, eps=1e-
     contiguous (q_out, k_out), or writes the given ones (any strides; q and k themselves are
     allowed). Rows of a position outside the table are left as they were (-1 marks padding,
     another one is recorded in the device status)."""
-    _expect(cos, "cos", (torch.float32,), (2,))
-    shape = _norm_shape(q, k, cos, positions)
-    _expect_table(cos, sin, q.shape[3])
-    f32 = _expect_weights(q_weight, k_weight, q.dtype, q.shape[3])
-    pb = _expect_positions(positions, q.shape[0], q.shape[2])
-    if q_out is not None:
-        _expect(q_out, "q_out", (q.dtype,), (4,), tuple(q.shape))
-    if k_out is not None:
-        _expect(k_out, "k_out", (k.dtype,), (4,), tuple(k.shape))
-    hq, hk = _heads(q, "q"), _heads(k, "k")
-    _same_device(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out)
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    _call_on(q.device, "bsa_qk_norm_rotation", hq, hk, shape, _ptr(q_weight), _ptr(k_weight), f32,
-             _ptr(cos), _ptr(sin), cos.shape[0], _ptr(positions), pb, float(eps),
-             1 if interleaved else 0, _heads(q_out, "q_out", True), _heads(k_out, "k_out", True),
-             _stream(q.device))
-    return q_out, k_out
-
-
-def _like_layout(t):
-    """An empty tensor of t's shape, token-major in memory where t is, else contiguous."""
-    B, H, S, D = t.shape
-    if H > 1 and S > 1 and t.stride(1) < t.stride(2):
-        return torch.empty((B, S, H, D), dtype=t.dtype, device=t.device).transpose(1, 2)
-    return torch.empty((B, H, S, D), dtype=t.dtype, device=t.device)
+    return _lib.native().qk_norm_rotation(q, k, q_weight, k_weight, cos, sin, positions, eps,
+                                          interleaved, q_out, k_out)
 
 
 def qk_norm_rotation_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, positions=None,
@@ -598,42 +499,8 @@ def qk_norm_rotation_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin
     laid out as q and k are (token-major or contiguous); the weight gradients are fp32, summed
     over batch, heads and tokens in a fixed order. Rows that the forward call skips get
     zero gradients."""
-    _expect(cos, "cos", (torch.float32,), (2,))
-    shape = _norm_shape(q, k, cos, positions)
-    _expect_table(cos, sin, q.shape[3])
-    f32 = _expect_weights(q_weight, k_weight, q.dtype, q.shape[3])
-    pb = _expect_positions(positions, q.shape[0], q.shape[2])
-    _expect(dq_out, "dq_out", (q.dtype,), (4,), tuple(q.shape))
-    _expect(dk_out, "dk_out", (k.dtype,), (4,), tuple(k.shape))
-    _expect_workspace(workspace)
-    hs = [_heads(t, n) for t, n in ((dq_out, "dq_out"), (dk_out, "dk_out"), (q, "q"), (k, "k"))]
-    _same_device(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, positions, workspace)
-    need = _lib.load().bsa_qk_norm_rotation_workspace_bytes(shape)
-    if workspace is None or workspace.numel() < need:
-        workspace = _workspace(need, q.device)
-    dq, dk = _like_layout(q), _like_layout(k)
-    D = q.shape[3]
-    dw = torch.empty((2, D), dtype=torch.float32, device=q.device)
-    _call_on(q.device, "bsa_qk_norm_rotation_backward", *hs, shape, _ptr(q_weight), _ptr(k_weight),
-             f32, _ptr(cos), _ptr(sin), cos.shape[0], _ptr(positions), pb, float(eps),
-             1 if interleaved else 0, _heads(dq, "dq", True), _heads(dk, "dk", True), _ptr(dw[0]),
-             _ptr(dw[1]), _ptr(workspace), workspace.numel(), _stream(q.device))
-    return dq, dk, dw[0], dw[1]
-
-
-def _expect_i32(t, name, shape):
-    _expect(t, name, (torch.int32,), (len(shape),), shape)
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-
-
-def _expect_block_table(block_table, R):
-    _expect(block_table, "block_table", (torch.int32,), (2,))
-    if block_table.shape[0] != R:
-        raise ValueError(f"block_table: {block_table.shape[0]} rows for {R} requests")
-    if block_table.numel() and block_table.shape[1] > 1 and block_table.stride(1) != 1:
-        raise ValueError("block_table: rows must be contiguous")
-    return block_table.stride(0) if R > 1 else block_table.shape[1]
+    return _lib.native().qk_norm_rotation_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos,
+                                                   sin, positions, eps, interleaved, workspace)
 
 
 def paged_block_tables(context_lens, new_lens, block_table, free_pages, n_tokens, page_size,
@@ -646,52 +513,8 @@ def paged_block_tables(context_lens, new_lens, block_table, free_pages, n_tokens
     of every new token, request by request (-1 behind the last), the running sums of the new
     lengths, and the number of pages needed. Where that is more than ``free_pages`` holds,
     the pages that it lacks, and the slots of their tokens, are -1."""
-    _expect(context_lens, "context_lens", (torch.int32,), (1,))
-    R = context_lens.shape[0]
-    _expect_i32(context_lens, "context_lens", (R,))
-    _expect_i32(new_lens, "new_lens", (R,))
-    stride = _expect_block_table(block_table, R)
-    _expect(free_pages, "free_pages", (torch.int32,), (1,))
-    _expect_i32(free_pages, "free_pages", tuple(free_pages.shape))
-    if R > 1 and block_table.shape[1] > 0 and stride < block_table.shape[1]:
-        raise ValueError("block_table: rows may not overlap")
-    _same_device(context_lens, new_lens, block_table, free_pages)
-    T, dev = int(n_tokens), context_lens.device
-    if T < 0:
-        raise ValueError("n_tokens < 0")
-    pad = (T + 3) // 4 * 4  # both maps start on 16-byte boundaries of one allocation
-    buf = torch.empty(2 * pad + R + 2, dtype=torch.int32, device=dev)
-    slots, positions = buf[:T], buf[pad:pad + T]
-    cu_new, taken = buf[2 * pad:2 * pad + R + 1], buf[2 * pad + R + 1:]
-    _call_on(dev, "bsa_paged_block_tables", _ptr(context_lens), _ptr(new_lens), R, _ptr(block_table),
-             block_table.shape[1], stride, _ptr(free_pages), free_pages.shape[0], T, int(page_size),
-             int(n_pages), _ptr(slots), _ptr(positions), _ptr(cu_new), _ptr(taken), _stream(dev))
-    return slots, positions, cu_new, taken
-
-
-def _paged_cache(k_cache, v_cache, Hkv=None, D=None, dtype=None, written=False):
-    """bsa_paged_cache of k_cache and v_cache (n_pages, Hkv, page, D), bf16 or fp16, any strides
-    that are multiples of 16 bytes."""
-    _expect(k_cache, "k_cache", tuple(_DT_PAGED) if dtype is None else (dtype,), (4,))
-    if k_cache.dtype not in _DT_PAGED:
-        raise ValueError(f"k_cache: dtype {k_cache.dtype}, expected one of {list(_DT_PAGED)}")
-    _expect(v_cache, "v_cache", (k_cache.dtype,), (4,), tuple(k_cache.shape))
-    n, H, P, Dc = k_cache.shape
-    if (Hkv is not None and H != Hkv) or (D is not None and Dc != D):
-        raise ValueError(f"k_cache: shape {tuple(k_cache.shape)}, expected (pages, {Hkv}, page, {D})")
-    if min(k_cache.shape) < 1:
-        raise ValueError(f"k_cache: empty, shape {tuple(k_cache.shape)}")
-    c = _lib.PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), n, P, H, Dc, _DT_PAGED[k_cache.dtype])
-    for t, x in ((k_cache, "k"), (v_cache, "v")):
-        if t.stride(3) != 1:
-            raise ValueError(f"{x}_cache: the last dimension must be contiguous")
-        if t.data_ptr() % 16 or any(s % 8 for s, m in zip(t.stride()[:3], t.shape) if m > 1):
-            raise ValueError(f"{x}_cache: pointer and strides must be multiples of 16 bytes")
-        if any(s <= 0 for s, m in zip(t.stride()[:3], t.shape) if m > 1):
-            raise ValueError(f"{x}_cache: may not be broadcast")
-        for s, m, name in zip(t.stride(), t.shape, ("page", "head", "row")):
-            setattr(c, f"{x}_{name}_stride", s if m > 1 else 8)  # unused for one entry
-    return c
+    return _lib.native().paged_block_tables(context_lens, new_lens, block_table, free_pages,
+                                            n_tokens, page_size, n_pages)
 
 
 def paged_qk_norm_append(q, k, v, q_weight, k_weight, cos, sin, positions, slots, k_cache, v_cache,
@@ -699,53 +522,19 @@ def paged_qk_norm_append(q, k, v, q_weight, k_weight, cos, sin, positions, slots
     """``qk_norm_rotation`` of packed new tokens, q (Hq,T,D), k and v (Hkv,T,D), with the
     keys written into ``k_cache`` and the values into ``v_cache`` (n_pages, Hkv, page, D) at
     ``slots`` (int32 (T,), -1: not written), as ``paged_block_tables`` gives them with
-    ``positions`` (-1: the token is skipped). bf16 or fp16. Returns q_out (Hq,T,D)."""
-    _expect(q, "q", tuple(_DT_PAGED), (3,))
-    Hq, T, D = q.shape
-    _expect(k, "k", (q.dtype,), (3,))
-    if k.shape[1] != T or k.shape[2] != D or k.shape[0] <= 0:
-        raise ValueError(f"k: shape {tuple(k.shape)} does not fit q {tuple(q.shape)}")
-    _expect(v, "v", (q.dtype,), (3,), tuple(k.shape))
-    _expect_table(cos, sin, D)
-    f32 = _expect_weights(q_weight, k_weight, q.dtype, D)
-    _expect_i32(positions, "positions", (T,))
-    _expect_i32(slots, "slots", (T,))
-    cache = _paged_cache(k_cache, v_cache, k.shape[0], D, q.dtype)
-    if q_out is not None:
-        _expect(q_out, "q_out", (q.dtype,), (3,), tuple(q.shape))
-    hq, hk, hv = _heads(q, "q"), _heads(k, "k"), _heads(v, "v")
-    _same_device(q, k, v, q_weight, k_weight, cos, sin, positions, slots, k_cache, v_cache, q_out)
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _call_on(q.device, "bsa_paged_qk_norm_append", hq, hk, hv, T, Hq, _ptr(q_weight), _ptr(k_weight),
-             f32, _ptr(cos), _ptr(sin), cos.shape[0], _ptr(positions), _ptr(slots), float(eps),
-             1 if interleaved else 0, _heads(q_out, "q_out", True), cache, _stream(q.device))
-    return q_out
+    ``positions`` (-1: the token is skipped). bf16 or fp16; caches of any strides that are
+    multiples of 16 bytes. Returns q_out (Hq,T,D)."""
+    return _lib.native().paged_qk_norm_append(q, k, v, q_weight, k_weight, cos, sin, positions,
+                                              slots, k_cache, v_cache, eps, interleaved, q_out)
 
 
-def _page_mask_strides(page_mask, R, Hkv, width):
-    """bool/uint8 (R, pages) or (R, Hkv, pages) (size-1 leading dimensions broadcast) ->
-    (uint8 tensor, request stride, head stride)."""
-    m = page_mask
-    if m.dtype == torch.bool:
-        m = m.view(torch.uint8)
-    if m.dtype != torch.uint8 or m.dim() not in (2, 3):
-        raise ValueError("page_mask must be bool or uint8 with 2 or 3 dimensions")
-    if m.dim() == 2:
-        m = m[:, None]
-    if m.shape[0] not in (1, R) or m.shape[1] not in (1, Hkv) or m.shape[2] != width:
-        raise ValueError(f"page_mask: shape {tuple(page_mask.shape)}, expected ({R}, {Hkv}, {width}) "
-                         f"or ({R}, {width})")
-    if width > 1 and m.stride(2) != 1:
-        m = m.contiguous()
-    return m, m.stride(0) if m.shape[0] > 1 else 0, m.stride(1) if m.shape[1] > 1 else 0
-
-
-def paged_attention_workspace_bytes(q, k_cache, v_cache, block_table, max_new=None):
+def paged_attention_workspace_bytes(q, k_cache, block_table, max_new=None):
     """Workspace of ``paged_chunk_attention`` for these tensors."""
+    n, Hkv, page, D = k_cache.shape
+    cache = _lib.PagedCache(256, 256, n, page, Hkv, D, _DT_PAGED[k_cache.dtype])
+    R, width = block_table.shape
     return _lib.load().bsa_paged_attention_workspace_bytes(
-        _paged_cache(k_cache, v_cache), block_table.shape[0], q.shape[1], q.shape[0],
-        q.shape[1] if max_new is None else int(max_new), block_table.shape[1])
+        cache, R, q.shape[1], q.shape[0], q.shape[1] if max_new is None else int(max_new), width)
 
 
 def paged_chunk_attention(q, k_cache, v_cache, block_table, cu_new, context_lens, causal=True,
@@ -758,32 +547,6 @@ def paged_chunk_attention(q, k_cache, v_cache, block_table, cu_new, context_lens
     ``page_mask`` bool/uint8 (R, width) or (R, Hkv, width) keeps the pages that are not zero,
     shared by a KV head's query heads; a row that no key is left for gets 0. bf16 or fp16,
     D in {64, 128}. Returns q's type (Hq,T,D); rows from ``cu_new[R]`` on are not written."""
-    _expect(q, "q", tuple(_DT_PAGED), (3,))
-    Hq, T, D = q.shape
-    _expect(block_table, "block_table", (torch.int32,), (2,))
-    R, width = block_table.shape
-    stride = _expect_block_table(block_table, R)
-    _expect_i32(cu_new, "cu_new", (R + 1,))
-    _expect_i32(context_lens, "context_lens", (R,))
-    cache = _paged_cache(k_cache, v_cache, None, D, q.dtype)
-    if Hq % cache.Hkv:
-        raise ValueError(f"q: {Hq} heads, not a multiple of the cache's {cache.Hkv}")
-    m, mr, mg = (None, 0, 0) if page_mask is None else _page_mask_strides(page_mask, R, cache.Hkv, width)
-    if out is not None:
-        _expect(out, "out", (q.dtype,), (3,), tuple(q.shape))
-    _expect_workspace(workspace)
-    hq = _heads(q, "q")
-    _same_device(q, k_cache, v_cache, block_table, cu_new, context_lens, m, out, workspace)
-    max_new = T if max_new is None else int(max_new)
-    need = _lib.load().bsa_paged_attention_workspace_bytes(cache, R, T, Hq, max_new, width)
-    if need == 0:
-        raise _lib.BsaError("bsa_paged_attention_workspace_bytes", _lib.BSA_ERR_UNSUPPORTED, _lib.detail())
-    if out is None:
-        out = torch.empty((Hq, T, D), dtype=q.dtype, device=q.device)
-    if workspace is None or workspace.numel() < need:
-        workspace = _workspace(need, q.device)
-    _call_on(q.device, "bsa_paged_chunk_attention", hq, cache, _ptr(block_table), width, stride,
-             _ptr(cu_new), _ptr(context_lens), R, T, Hq, max_new, _ptr(m), mr, mg,
-             float(scale or 0.0), 1 if causal else 0, _heads(out, "out", True), _ptr(workspace),
-             workspace.numel(), _stream(q.device))
-    return out
+    return _lib.native().paged_chunk_attention(q, k_cache, v_cache, block_table, cu_new,
+                                               context_lens, causal, max_new, page_mask, scale,
+                                               out, workspace)
