@@ -168,23 +168,23 @@ struct HeadsOut {
   int64_t sb, sh, ss;
 };
 
+// The heads of a call are cut into runs, each inside one section (queries, keys, and the
+// values of the paged form); grid (token groups, runs).
 struct NormArgs {
-  HeadsIn q, k, v;
-  HeadsOut qo, ko;
-  int B, S, Hq, Hkv;
-  int heads;      // rows of a token: Hq + Hkv (+ Hkv values for the paged form)
-  int per_group;  // heads that one lane group walks over
-  const void *qw, *kw;
+  HeadsIn x[3];
+  HeadsOut y[3];      // of a paged section: sb = page stride, sh = head stride, ss = row stride
+  int heads[3];       // 0 values without a cache
+  int first_run[3];   // first run of the keys and of the values in [1], [2]
+  int per_run;
+  int B, S;
+  const void* w[2];
   int w_f32;
   const float *cos, *sin;
   int n_pos;
   const int32_t* positions;
   int64_t pos_b;
   float eps;
-  // paged destination of keys and values
-  const int32_t* slots;
-  void *kc, *vc;
-  int64_t kp, kh, kr, vp, vh, vr;
+  const int32_t* slots;  // paged form: destination of the keys and values
   int page_shift, n_slots;
 };
 
@@ -198,7 +198,15 @@ __device__ __forceinline__ int checked_position(const int32_t* positions, int64_
 
 constexpr int kNormSite = 120;
 
-// One lane group per (token, run of per_group heads); grid (token groups, head runs).
+template <int D>
+__device__ __forceinline__ void load_angles(const float* cos, const float* sin, int pos, int l,
+                                            float (&c)[4], float (&s)[4]) {
+  const float4 c4 = *reinterpret_cast<const float4*>(cos + static_cast<int64_t>(pos) * (D / 2) + 4 * l);
+  const float4 s4 = *reinterpret_cast<const float4*>(sin + static_cast<int64_t>(pos) * (D / 2) + 4 * l);
+  c[0] = c4.x; c[1] = c4.y; c[2] = c4.z; c[3] = c4.w;
+  s[0] = s4.x; s[1] = s4.y; s[2] = s4.z; s[3] = s4.w;
+}
+
 template <typename T, int D, bool INTER, bool PAGED>
 __global__ void __launch_bounds__(kNormThreads) norm_rotation_kernel(const NormArgs a) {
   constexpr int L = D / 8;
@@ -208,69 +216,65 @@ __global__ void __launch_bounds__(kNormThreads) norm_rotation_kernel(const NormA
   const int64_t ntok = static_cast<int64_t>(a.B) * a.S;
   const bool in = tok < ntok;
   const int b = in ? static_cast<int>(tok / a.S) : 0, s = in ? static_cast<int>(tok % a.S) : 0;
+  const int run = blockIdx.y;
+  const int sec = PAGED && run >= a.first_run[2] ? 2 : (run >= a.first_run[1] ? 1 : 0);
+  const int h_begin = (run - (sec ? a.first_run[sec] : 0)) * a.per_run;
+  const int h_end = min(a.heads[sec], h_begin + a.per_run);
+  const T* src = static_cast<const T*>(a.x[sec].p) + b * a.x[sec].sb + s * a.x[sec].ss;
+  const int64_t xsh = a.x[sec].sh, ysh = a.y[sec].sh;
+
+  Raw<T> cur[kUnroll], nxt[kUnroll];
+  // rows of a token behind the last one, or of a head behind the run's, are not read
+  auto load = [&](Raw<T>(&r)[kUnroll], int h0) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (in && h0 + u < h_end) r[u] = load_row<T, D, INTER>(src + (h0 + u) * xsh, l);
+      else r[u] = Raw<T>{};
+    }
+  };
+  load(cur, h_begin);
+
   int pos = in ? checked_position(a.positions, a.pos_b, b, s, a.n_pos) : -1;
   if (pos == -2 && l == 0) report_device_error(kStatusBadLabel, kNormSite);
-  const bool live = pos >= 0;
+  bool put = pos >= 0;
   if (pos < 0) pos = 0;
-  int64_t kdst = 0, vdst = 0;
-  bool put = false;
-  if constexpr (PAGED) {
-    const int slot = live ? a.slots[s] : -1;
-    put = slot >= 0 && slot < a.n_slots;
-    if (live && !put && slot != -1 && l == 0) report_device_error(kStatusBadLabel, kNormSite + 1);
-    if (put) {
-      const int64_t page = slot >> a.page_shift, row = slot & ((1 << a.page_shift) - 1);
-      kdst = page * a.kp + row * a.kr;
-      vdst = page * a.vp + row * a.vr;
+  T* dst = static_cast<T*>(a.y[sec].p);
+  if (PAGED && sec > 0) {
+    const int slot = put ? a.slots[s] : -1;
+    const bool fits = slot >= 0 && slot < a.n_slots;
+    if (put && !fits && slot != -1 && l == 0) report_device_error(kStatusBadLabel, kNormSite + 1);
+    put = put && fits;
+    if (put)
+      dst += static_cast<int64_t>(slot >> a.page_shift) * a.y[sec].sb +
+             static_cast<int64_t>(slot & ((1 << a.page_shift) - 1)) * a.y[sec].ss;
+  } else {
+    dst += b * a.y[sec].sb + s * a.y[sec].ss;
+  }
+  if (PAGED && sec == 2) {  // values are copied (the conversion there and back is exact)
+#pragma unroll 1
+    for (int h0 = h_begin; h0 < h_end; h0 += kUnroll) {
+      load(nxt, h0 + kUnroll);
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        float x[4], y[4];
+        to_pairs<T, INTER>(cur[u], x, y);
+        if (put && h0 + u < h_end) store_row<T, D, INTER>(dst + (h0 + u) * ysh, l, x, y);
+        cur[u] = nxt[u];
+      }
     }
+    return;
   }
-  float c[4] = {}, sn[4] = {};
-  if (live) {
-    const float4 c4 = *reinterpret_cast<const float4*>(a.cos + static_cast<int64_t>(pos) * (D / 2) + 4 * l);
-    const float4 s4 = *reinterpret_cast<const float4*>(a.sin + static_cast<int64_t>(pos) * (D / 2) + 4 * l);
-    c[0] = c4.x; c[1] = c4.y; c[2] = c4.z; c[3] = c4.w;
-    sn[0] = s4.x; sn[1] = s4.y; sn[2] = s4.z; sn[3] = s4.w;
-  }
-  const int h_begin = blockIdx.y * a.per_group;
-  const int h_end = min(a.heads, h_begin + a.per_group);
-  const T* qrow = static_cast<const T*>(a.q.p) + b * a.q.sb + s * a.q.ss;
-  const T* krow = static_cast<const T*>(a.k.p) + b * a.k.sb + s * a.k.ss;
-  const T* vrow = static_cast<const T*>(a.v.p) + s * a.v.ss;
-  T* qdst = static_cast<T*>(a.qo.p) + b * a.qo.sb + s * a.qo.ss;
-  T* kodst = PAGED ? static_cast<T*>(a.kc) + kdst : static_cast<T*>(a.ko.p) + b * a.ko.sb + s * a.ko.ss;
-  T* vodst = static_cast<T*>(a.vc) + vdst;
-  const int64_t kosh = PAGED ? a.kh : a.ko.sh;
-  const bool put_k = PAGED ? put : live;
-
-  float wa[4], wb[4];
-  bool q_weight = h_begin < a.Hq;
-  load_weight<T, D, INTER>(q_weight ? a.qw : a.kw, a.w_f32, l, wa, wb);
+  float c[4] = {}, sn[4] = {}, wa[4], wb[4];
+  if (put) load_angles<D>(a.cos, a.sin, pos, l, c, sn);
+  load_weight<T, D, INTER>(a.w[sec], a.w_f32, l, wa, wb);
 #pragma unroll 1
   for (int h0 = h_begin; h0 < h_end; h0 += kUnroll) {
-    Raw<T> raw[kUnroll];
+    load(nxt, h0 + kUnroll);  // on their way while these rows are worked on
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u;
-      const T* row = h < a.Hq ? qrow + h * a.q.sh
-                              : (h < a.Hq + a.Hkv ? krow + (h - a.Hq) * a.k.sh
-                                                  : vrow + (h - a.Hq - a.Hkv) * a.v.sh);
-      if (live && h < h_end) raw[u] = load_row<T, D, INTER>(row, l);
-      else raw[u] = Raw<T>{};
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u;
       float x[4], y[4];
-      to_pairs<T, INTER>(raw[u], x, y);
-      if (PAGED && h >= a.Hq + a.Hkv) {  // a value: copied (the conversion there and back is exact)
-        if (put && h < h_end)
-          store_row<T, D, INTER>(vodst + (h - a.Hq - a.Hkv) * a.vh, l, x, y);
-        continue;
-      }
-      if (q_weight && h >= a.Hq) {
-        load_weight<T, D, INTER>(a.kw, a.w_f32, l, wa, wb);
-        q_weight = false;
-      }
+      to_pairs<T, INTER>(cur[u], x, y);
+      cur[u] = nxt[u];
       float ss = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
@@ -282,13 +286,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_rotation_kernel(const NormA
         o0[i] = ya * c[i] - yb * sn[i];
         o1[i] = ya * sn[i] + yb * c[i];
       }
-      if (h < h_end) {
-        if (h < a.Hq) {
-          if (live) store_row<T, D, INTER>(qdst + h * a.qo.sh, l, o0, o1);
-        } else if (put_k) {
-          store_row<T, D, INTER>(kodst + (h - a.Hq) * kosh, l, o0, o1);
-        }
-      }
+      if (put && h0 + u < h_end) store_row<T, D, INTER>(dst + (h0 + u) * ysh, l, o0, o1);
     }
   }
 }
@@ -296,8 +294,10 @@ __global__ void __launch_bounds__(kNormThreads) norm_rotation_kernel(const NormA
 struct NormBackArgs {
   HeadsIn x[2], dy[2];  // queries, keys
   HeadsOut dx[2];
-  int B, S, Hq, Hkv;
-  int per_group, head_runs;
+  int heads[2];
+  int ctas[2];      // CTAs of each side: queries first in the grid
+  int per_run;      // heads that one lane group walks over
+  int B, S;
   const void* w[2];
   int w_f32;
   const float *cos, *sin;
@@ -305,136 +305,131 @@ struct NormBackArgs {
   const int32_t* positions;
   int64_t pos_b;
   float eps;
-  float* part;  // (CTAs, 2, D) weight-gradient sums
+  float* part;  // (CTAs, D) weight-gradient sums
 };
 
-// Units (token group, run of per_group heads) are taken in a fixed stride over the grid, so
-// a CTA's share of the weight sums, and the order inside it, depend on the sizes alone.
+// A CTA belongs to one side and takes that side's units (token group, run of heads) in a fixed
+// stride, so its share of the weight sums, and the order inside it, depend on the sizes alone.
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(kNormThreads) norm_rotation_back_kernel(const NormBackArgs a) {
   constexpr int L = D / 8, kGroups = kNormThreads / L;
   constexpr int kUnroll = 2;
   const int l = threadIdx.x % L, grp = threadIdx.x / L;
+  const int side = blockIdx.x >= a.ctas[0] ? 1 : 0;
   const int64_t ntok = static_cast<int64_t>(a.B) * a.S;
   const int64_t tgroups = (ntok + kGroups - 1) / kGroups;
-  const int heads = a.Hq + a.Hkv;
-  float dwa[2][4] = {}, dwb[2][4] = {};
-  float wa[2][4], wb[2][4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) load_weight<T, D, INTER>(a.w[i], a.w_f32, l, wa[i], wb[i]);
+  const int runs = (a.heads[side] + a.per_run - 1) / a.per_run;
+  const int64_t xsh = a.x[side].sh, gsh = a.dy[side].sh, dsh = a.dx[side].sh;
+  float dwa[4] = {}, dwb[4] = {}, wa[4], wb[4];
+  load_weight<T, D, INTER>(a.w[side], a.w_f32, l, wa, wb);
 #pragma unroll 1
-  for (int64_t u = blockIdx.x; u < tgroups * a.head_runs; u += gridDim.x) {
-    const int64_t tok = (u / a.head_runs) * kGroups + grp;
-    const int run = static_cast<int>(u % a.head_runs);
+  for (int64_t u = blockIdx.x - (side ? a.ctas[0] : 0); u < tgroups * runs; u += a.ctas[side]) {
+    // runs change slowest: the CTAs work on neighbouring tokens of the same heads
+    const int64_t tok = (u % tgroups) * kGroups + grp;
+    const int run = static_cast<int>(u / tgroups);
     const bool in = tok < ntok;
     const int b = in ? static_cast<int>(tok / a.S) : 0, s = in ? static_cast<int>(tok % a.S) : 0;
+    const int h_begin = run * a.per_run, h_end = min(a.heads[side], h_begin + a.per_run);
+    const T* xrow = static_cast<const T*>(a.x[side].p) + b * a.x[side].sb + s * a.x[side].ss;
+    const T* grow = static_cast<const T*>(a.dy[side].p) + b * a.dy[side].sb + s * a.dy[side].ss;
+    T* drow = static_cast<T*>(a.dx[side].p) + b * a.dx[side].sb + s * a.dx[side].ss;
+    Raw<T> rx[kUnroll], rg[kUnroll], nx[kUnroll], ng[kUnroll];
+    auto load = [&](Raw<T>(&x)[kUnroll], Raw<T>(&g)[kUnroll], int h0) {
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) {
+        x[j] = g[j] = Raw<T>{};
+        if (in && h0 + j < h_end) {
+          x[j] = load_row<T, D, INTER>(xrow + (h0 + j) * xsh, l);
+          g[j] = load_row<T, D, INTER>(grow + (h0 + j) * gsh, l);
+        }
+      }
+    };
+    load(rx, rg, h_begin);
     int pos = in ? checked_position(a.positions, a.pos_b, b, s, a.n_pos) : -1;
     if (pos == -2 && l == 0) report_device_error(kStatusBadLabel, kNormSite + 2);
     const bool live = pos >= 0;
-    if (pos < 0) pos = 0;
     float c[4] = {}, sn[4] = {};
-    if (live) {
-      const float4 c4 = *reinterpret_cast<const float4*>(a.cos + static_cast<int64_t>(pos) * (D / 2) + 4 * l);
-      const float4 s4 = *reinterpret_cast<const float4*>(a.sin + static_cast<int64_t>(pos) * (D / 2) + 4 * l);
-      c[0] = c4.x; c[1] = c4.y; c[2] = c4.z; c[3] = c4.w;
-      sn[0] = s4.x; sn[1] = s4.y; sn[2] = s4.z; sn[3] = s4.w;
-    }
-    const int h_begin = run * a.per_group, h_end = min(heads, h_begin + a.per_group);
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {  // queries, then keys of the run
-      const int lo = side ? max(h_begin, a.Hq) - a.Hq : h_begin;
-      const int hi = side ? h_end - a.Hq : min(h_end, a.Hq);
-      const T* xrow = static_cast<const T*>(a.x[side].p) + b * a.x[side].sb + s * a.x[side].ss;
-      const T* grow = static_cast<const T*>(a.dy[side].p) + b * a.dy[side].sb + s * a.dy[side].ss;
-      T* drow = static_cast<T*>(a.dx[side].p) + b * a.dx[side].sb + s * a.dx[side].ss;
+    if (live) load_angles<D>(a.cos, a.sin, pos, l, c, sn);
 #pragma unroll 1
-      for (int h0 = lo; h0 < hi; h0 += kUnroll) {
-        Raw<T> rx[kUnroll], rg[kUnroll];
+    for (int h0 = h_begin; h0 < h_end; h0 += kUnroll) {
+      load(nx, ng, h0 + kUnroll);
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-          rx[j] = rg[j] = Raw<T>{};
-          if (live && h0 + j < hi) {
-            rx[j] = load_row<T, D, INTER>(xrow + (h0 + j) * a.x[side].sh, l);
-            rg[j] = load_row<T, D, INTER>(grow + (h0 + j) * a.dy[side].sh, l);
-          }
+      for (int j = 0; j < kUnroll; ++j) {
+        float xa[4], xb[4], ga[4], gb[4], za[4], zb[4];
+        to_pairs<T, INTER>(rx[j], xa, xb);
+        to_pairs<T, INTER>(rg[j], ga, gb);
+        rx[j] = nx[j];
+        rg[j] = ng[j];
+        if (!live) {  // a skipped row: zero gradients, nothing in the sums
+#pragma unroll
+          for (int i = 0; i < 4; ++i) xa[i] = xb[i] = ga[i] = gb[i] = 0.f;
         }
+        float ss = 0.f, dot = 0.f;
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-          float xa[4], xb[4], ga[4], gb[4], za[4], zb[4];
-          to_pairs<T, INTER>(rx[j], xa, xb);
-          to_pairs<T, INTER>(rg[j], ga, gb);
-          float ss = 0.f, dot = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            za[i] = ga[i] * c[i] + gb[i] * sn[i];
-            zb[i] = gb[i] * c[i] - ga[i] * sn[i];
-            ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
-            dot = fmaf(za[i] * wa[side][i], xa[i], fmaf(zb[i] * wb[side][i], xb[i], dot));
-          }
-          ss = row_sum<D>(ss);
-          dot = row_sum<D>(dot);
-          const float r = rsqrtf(ss * (1.f / D) + a.eps);
-          const float k = r * r * dot * (1.f / D);
-          float oa[4], ob[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            dwa[side][i] = fmaf(za[i] * r, xa[i], dwa[side][i]);
-            dwb[side][i] = fmaf(zb[i] * r, xb[i], dwb[side][i]);
-            oa[i] = r * (za[i] * wa[side][i] - xa[i] * k);
-            ob[i] = r * (zb[i] * wb[side][i] - xb[i] * k);
-          }
-          if (in && h0 + j < hi) {
-            if (!live) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) oa[i] = ob[i] = 0.f;
-            }
-            store_row<T, D, INTER>(drow + (h0 + j) * a.dx[side].sh, l, oa, ob);
-          }
+        for (int i = 0; i < 4; ++i) {
+          za[i] = ga[i] * c[i] + gb[i] * sn[i];
+          zb[i] = gb[i] * c[i] - ga[i] * sn[i];
+          ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
+          dot = fmaf(za[i] * wa[i], xa[i], fmaf(zb[i] * wb[i], xb[i], dot));
         }
+        ss = row_sum<D>(ss);
+        dot = row_sum<D>(dot);
+        const float r = live ? rsqrtf(ss * (1.f / D) + a.eps) : 0.f;
+        const float k = r * r * dot * (1.f / D);
+        float oa[4], ob[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dwa[i] = fmaf(za[i] * r, xa[i], dwa[i]);
+          dwb[i] = fmaf(zb[i] * r, xb[i], dwb[i]);
+          oa[i] = r * (za[i] * wa[i] - xa[i] * k);
+          ob[i] = r * (zb[i] * wb[i] - xb[i] * k);
+        }
+        if (in && h0 + j < h_end) store_row<T, D, INTER>(drow + (h0 + j) * dsh, l, oa, ob);
       }
     }
   }
   // the lane groups' sums, added in group order
-  __shared__ float red[kGroups][2][D];
+  __shared__ float red[kGroups][D];
 #pragma unroll
-  for (int side = 0; side < 2; ++side)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int da = INTER ? 8 * l + 2 * i : 4 * l + i;
-      const int db = INTER ? da + 1 : D / 2 + 4 * l + i;
-      red[grp][side][da] = dwa[side][i];
-      red[grp][side][db] = dwb[side][i];
-    }
+  for (int i = 0; i < 4; ++i) {
+    const int da = INTER ? 8 * l + 2 * i : 4 * l + i;
+    const int db = INTER ? da + 1 : D / 2 + 4 * l + i;
+    red[grp][da] = dwa[i];
+    red[grp][db] = dwb[i];
+  }
   __syncthreads();
-  for (int e = threadIdx.x; e < 2 * D; e += kNormThreads) {
+  if (threadIdx.x < D) {
     float t = 0.f;
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) t += red[g][e / D][e % D];
-    a.part[static_cast<size_t>(blockIdx.x) * 2 * D + e] = t;
+    for (int g = 0; g < kGroups; ++g) t += red[g][threadIdx.x];
+    a.part[static_cast<size_t>(blockIdx.x) * D + threadIdx.x] = t;
   }
 }
 
-// Sum of the CTAs' shares, one CTA per 32 columns of the (2, D) sums: warp w adds shares
-// w, w + 32, ... and the warps' sums are added in order, in fp64 (hundreds of shares with
-// cancelling signs).
-__global__ void __launch_bounds__(1024) norm_weight_sum_kernel(const float* __restrict__ part,
-                                                               int n, int D, float* __restrict__ dqw,
+// Sum of the CTAs' shares; grid (D / 32, sides): warp w adds the side's shares w, w + 32, ...
+// and the warps' sums are added in order, in fp64 (hundreds of shares with cancelling signs).
+__global__ void __launch_bounds__(1024) norm_weight_sum_kernel(const float* __restrict__ part, int nq,
+                                                               int nk, int D, float* __restrict__ dqw,
                                                                float* __restrict__ dkw) {
   __shared__ double red[32][33];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, side = blockIdx.y;
   const int col = blockIdx.x * 32 + lane;
+  const float* p = part + (side ? static_cast<size_t>(nq) * D : 0) + col;
+  const int n = side ? nk : nq;
   double t = 0.0;
 #pragma unroll 4
-  for (int i = w; i < n; i += 32) t += static_cast<double>(part[static_cast<size_t>(i) * 2 * D + col]);
+  for (int i = w; i < n; i += 32) t += static_cast<double>(p[static_cast<size_t>(i) * D]);
   red[w][lane] = t;
   __syncthreads();
   if (w == 0) {
     double s = 0.0;
 #pragma unroll
     for (int i = 0; i < 32; ++i) s += red[i][lane];
-    (col < D ? dqw[col] : dkw[col - D]) = static_cast<float>(s);
+    (side ? dkw : dqw)[col] = static_cast<float>(s);
   }
 }
+
+constexpr int kNormBackCtas = 148 * 4;
 
 int norm_elem_bytes(int dtype) { return dtype == BSA_F32 ? 4 : 2; }
 
@@ -468,10 +463,10 @@ int check_norm_common(const bsa_shape& s, const void* qw, const void* kw, const 
 HeadsIn in_of(const bsa_heads& h) { return {h.ptr, h.stride_b, h.stride_h, h.stride_s}; }
 HeadsOut out_of(const bsa_heads& h) { return {h.ptr, h.stride_b, h.stride_h, h.stride_s}; }
 
-// Heads per lane group: a group walks over all heads of its token when the tokens alone
-// fill the GPU several times over, and over fewer, in whole steps of 4, when they do not.
-int heads_per_group(int64_t token_groups, int heads) {
-  constexpr int64_t kWant = 148 * 16;  // CTAs that keep every SM's loads in flight twice over
+// Heads of a run: a lane group walks over all heads of its token's section when the tokens
+// alone fill the GPU several times over, and over fewer, in whole steps of 4, when not.
+int heads_per_run(int64_t token_groups, int heads) {
+  constexpr int64_t kWant = 148 * 8;  // CTAs that give every SM its loads in flight
   const int64_t runs = std::min<int64_t>((heads + 3) / 4, std::max<int64_t>(1, kWant / std::max<int64_t>(token_groups, 1)));
   return static_cast<int>(((heads + runs - 1) / runs + 3) / 4 * 4);
 }
@@ -487,8 +482,10 @@ int launch_norm(NormArgs& a, int dtype, int D, int interleaved, cudaStream_t st)
   const int64_t ntok = static_cast<int64_t>(a.B) * a.S;
   const int per_cta = kNormThreads / (D / 8);
   const int64_t tg = (ntok + per_cta - 1) / per_cta;
-  a.per_group = heads_per_group(tg, a.heads);
-  const dim3 grid(static_cast<unsigned>(tg), ceil_div(a.heads, a.per_group));
+  a.per_run = heads_per_run(tg, a.heads[0] + a.heads[1] + a.heads[2]);
+  a.first_run[1] = ceil_div(a.heads[0], a.per_run);
+  a.first_run[2] = a.first_run[1] + ceil_div(a.heads[1], a.per_run);
+  const dim3 grid(static_cast<unsigned>(tg), a.first_run[2] + ceil_div(a.heads[2], a.per_run));
 #define BSA_NORM(T)                                                              \
   (D == 64 ? launch_norm_t<T, 64, PAGED>(a, grid, interleaved, st)               \
            : launch_norm_t<T, 128, PAGED>(a, grid, interleaved, st))
@@ -500,13 +497,18 @@ int launch_norm(NormArgs& a, int dtype, int D, int interleaved, cudaStream_t st)
   return check_cuda(cudaGetLastError(), "norm_rotation_kernel");
 }
 
-// CTAs of the backward pass: each leaves one share of the weight sums.
-int norm_back_ctas(const bsa_shape& s, int* per_group, int* head_runs) {
+// CTAs of the backward pass, by side in proportion to the heads: each leaves one share of its
+// side's weight sums.
+void norm_back_plan(const bsa_shape& s, int* per_run, int (&ctas)[2]) {
   const int per_cta = kNormThreads / (s.D / 8);
   const int64_t tg = (static_cast<int64_t>(s.B) * s.Sq + per_cta - 1) / per_cta;
-  *per_group = heads_per_group(tg, s.Hq + s.Hkv);
-  *head_runs = ceil_div(s.Hq + s.Hkv, *per_group);
-  return static_cast<int>(std::min<int64_t>(148 * 4, std::max<int64_t>(tg * *head_runs, 1)));
+  *per_run = heads_per_run(tg, s.Hq + s.Hkv);
+  const int h[2] = {s.Hq, s.Hkv};
+  for (int i = 0; i < 2; ++i) {
+    const int64_t units = std::max<int64_t>(1, tg * ceil_div(h[i], *per_run));
+    const int64_t share = std::max<int64_t>(1, static_cast<int64_t>(kNormBackCtas) * h[i] / (s.Hq + s.Hkv));
+    ctas[i] = static_cast<int>(std::min(units, share));
+  }
 }
 
 }  // namespace
@@ -529,17 +531,16 @@ int bsa_qk_norm_rotation(bsa_heads q, bsa_heads k, bsa_shape shape, const void* 
   if (!positions && shape.Sq > n_pos)
     return fail(BSA_ERR_INVALID_ARG, "%d tokens, %d positions in the table", shape.Sq, n_pos);
   NormArgs a{};
-  a.q = in_of(q);
-  a.k = in_of(k);
-  a.qo = out_of(q_out);
-  a.ko = out_of(k_out);
+  a.x[0] = in_of(q);
+  a.x[1] = in_of(k);
+  a.y[0] = out_of(q_out);
+  a.y[1] = out_of(k_out);
   a.B = shape.B;
   a.S = shape.Sq;
-  a.Hq = shape.Hq;
-  a.Hkv = shape.Hkv;
-  a.heads = shape.Hq + shape.Hkv;
-  a.qw = q_weight;
-  a.kw = k_weight;
+  a.heads[0] = shape.Hq;
+  a.heads[1] = shape.Hkv;
+  a.w[0] = q_weight;
+  a.w[1] = k_weight;
   a.w_f32 = weight_f32;
   a.cos = cos;
   a.sin = sin;
@@ -554,9 +555,9 @@ size_t bsa_qk_norm_rotation_workspace_bytes(bsa_shape shape) {
   if ((shape.D != 64 && shape.D != 128) || shape.B < 0 || shape.Sq < 0 || shape.Hq <= 0 ||
       shape.Hkv <= 0 || shape.Hq > 16384 || shape.Hkv > 16384)
     return 0;
-  int pg, hr;
-  return bsa::align_up(static_cast<size_t>(bsa::norm_back_ctas(shape, &pg, &hr)) * 2 * shape.D *
-                           sizeof(float), 256);
+  int per_run, ctas[2];
+  bsa::norm_back_plan(shape, &per_run, ctas);
+  return bsa::align_up(static_cast<size_t>(ctas[0] + ctas[1]) * shape.D * sizeof(float), 256);
 }
 
 int bsa_qk_norm_rotation_backward(bsa_heads dq_out, bsa_heads dk_out, bsa_heads q, bsa_heads k,
@@ -591,8 +592,8 @@ int bsa_qk_norm_rotation_backward(bsa_heads dq_out, bsa_heads dk_out, bsa_heads 
   a.dx[1] = out_of(dk);
   a.B = shape.B;
   a.S = shape.Sq;
-  a.Hq = shape.Hq;
-  a.Hkv = shape.Hkv;
+  a.heads[0] = shape.Hq;
+  a.heads[1] = shape.Hkv;
   a.w[0] = q_weight;
   a.w[1] = k_weight;
   a.w_f32 = weight_f32;
@@ -603,7 +604,8 @@ int bsa_qk_norm_rotation_backward(bsa_heads dq_out, bsa_heads dk_out, bsa_heads 
   a.pos_b = pos_b_stride;
   a.eps = eps;
   a.part = static_cast<float*>(workspace);
-  const int ctas = none ? 0 : norm_back_ctas(shape, &a.per_group, &a.head_runs);
+  if (!none) norm_back_plan(shape, &a.per_run, a.ctas);
+  const int ctas = a.ctas[0] + a.ctas[1];
   cudaStream_t cs = as_stream(stream);
   if (!none) {
 #define BSA_NORM_BACK(T)                                                                        \
@@ -619,7 +621,8 @@ int bsa_qk_norm_rotation_backward(bsa_heads dq_out, bsa_heads dk_out, bsa_heads 
     count_launch();
     if ((st = check_cuda(cudaGetLastError(), "norm_rotation_back_kernel")) != BSA_OK) return st;
   }
-  norm_weight_sum_kernel<<<2 * shape.D / 32, 1024, 0, cs>>>(a.part, ctas, shape.D, dq_weight, dk_weight);
+  norm_weight_sum_kernel<<<dim3(shape.D / 32, 2), 1024, 0, cs>>>(a.part, a.ctas[0], a.ctas[1], shape.D,
+                                                                  dq_weight, dk_weight);
   count_launch();
   return check_cuda(cudaGetLastError(), "norm_weight_sum_kernel");
 }
@@ -642,17 +645,18 @@ int bsa_paged_qk_norm_append(bsa_heads q, bsa_heads k, bsa_heads v, int T, int H
       (st = check_heads(v, cache.dtype, "v")) || (st = check_heads(q_out, cache.dtype, "q_out")))
     return st;
   NormArgs a{};
-  a.q = in_of(q);
-  a.k = in_of(k);
-  a.v = in_of(v);
-  a.qo = out_of(q_out);
+  a.x[0] = in_of(q);
+  a.x[1] = in_of(k);
+  a.x[2] = in_of(v);
+  a.y[0] = out_of(q_out);
+  a.y[1] = {cache.k, cache.k_page_stride, cache.k_head_stride, cache.k_row_stride};
+  a.y[2] = {cache.v, cache.v_page_stride, cache.v_head_stride, cache.v_row_stride};
   a.B = 1;
   a.S = T;
-  a.Hq = Hq;
-  a.Hkv = cache.Hkv;
-  a.heads = Hq + 2 * cache.Hkv;
-  a.qw = q_weight;
-  a.kw = k_weight;
+  a.heads[0] = Hq;
+  a.heads[1] = a.heads[2] = cache.Hkv;
+  a.w[0] = q_weight;
+  a.w[1] = k_weight;
   a.w_f32 = weight_f32;
   a.cos = cos;
   a.sin = sin;
@@ -660,14 +664,6 @@ int bsa_paged_qk_norm_append(bsa_heads q, bsa_heads k, bsa_heads v, int T, int H
   a.positions = positions;
   a.eps = eps;
   a.slots = slots;
-  a.kc = cache.k;
-  a.vc = cache.v;
-  a.kp = cache.k_page_stride;
-  a.kh = cache.k_head_stride;
-  a.kr = cache.k_row_stride;
-  a.vp = cache.v_page_stride;
-  a.vh = cache.v_head_stride;
-  a.vr = cache.v_row_stride;
   a.page_shift = __builtin_ctz(cache.page);
   a.n_slots = cache.n_pages * cache.page;
   return launch_norm<true>(a, cache.dtype, cache.D, interleaved, as_stream(stream));
