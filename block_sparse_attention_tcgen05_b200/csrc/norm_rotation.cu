@@ -308,58 +308,135 @@ struct NormBackArgs {
   float* part;  // (CTAs, D) weight-gradient sums
 };
 
+// Asynchronous copy of a lane's eight values to its own shared-memory slot (zeros when !ok).
+template <typename T, int D, bool INTER>
+__device__ __forceinline__ void async_row(uint32_t dst, const T* row, int l, bool ok) {
+  if constexpr (!INTER && sizeof(T) == 2) {
+    const int n = ok ? 8 : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(row + 4 * l), "r"(n) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst + 8), "l"(row + D / 2 + 4 * l), "r"(n)
+                 : "memory");
+  } else {
+    const int n = ok ? 16 : 0;
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * kNormThreads * 16),
+                   "l"(INTER ? row + 8 * l + 4 * i : row + (i ? D / 2 : 0) + 4 * l), "r"(n)
+                   : "memory");
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ Raw<T> read_slot(const uint8_t* p) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
+    const uint4 u = ld16(p + i * kNormThreads * 16);
+    r.w[4 * i] = u.x;
+    r.w[4 * i + 1] = u.y;
+    r.w[4 * i + 2] = u.z;
+    r.w[4 * i + 3] = u.w;
+  }
+  return r;
+}
+
+constexpr int kBackUnroll = 2;   // rows of a step
+constexpr int kBackAhead = 3;    // steps on their way
+
+template <typename T>
+constexpr int norm_back_smem() {
+  return kBackAhead * kBackUnroll * 2 * 8 * static_cast<int>(sizeof(T)) * kNormThreads;
+}
+
 // A CTA belongs to one side and takes that side's units (token group, run of heads) in a fixed
 // stride, so its share of the weight sums, and the order inside it, depend on the sizes alone.
+// The rows of kBackAhead steps are on their way to shared memory, across units, while one step
+// is worked on: each lane copies what it will read itself, so nothing synchronises, and the
+// bytes in flight cost no registers (holding one step ahead in registers ran at 71 % of the
+// HBM rate, with two CTAs of 120 registers per SM).
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(kNormThreads) norm_rotation_back_kernel(const NormBackArgs a) {
   constexpr int L = D / 8, kGroups = kNormThreads / L;
-  constexpr int kUnroll = 2;
+  constexpr int kUnroll = kBackUnroll, kRow = 8 * sizeof(T) * kNormThreads, kStep = 2 * kUnroll * kRow;
+  extern __shared__ __align__(16) uint8_t ring[];
   const int l = threadIdx.x % L, grp = threadIdx.x / L;
   const int side = blockIdx.x >= a.ctas[0] ? 1 : 0;
-  const int64_t ntok = static_cast<int64_t>(a.B) * a.S;
-  const int64_t tgroups = (ntok + kGroups - 1) / kGroups;
-  const int runs = (a.heads[side] + a.per_run - 1) / a.per_run;
-  const int64_t xsh = a.x[side].sh, gsh = a.dy[side].sh, dsh = a.dx[side].sh;
+  const int ntok = a.B * a.S;
+  const int tgroups = ntok / kGroups + (ntok % kGroups ? 1 : 0);
+  const int heads = a.heads[side];
+  const int units = tgroups * ((heads + a.per_run - 1) / a.per_run);
+  const int u0 = blockIdx.x - (side ? a.ctas[0] : 0);
+  const uint32_t slot0 = smem_u32(ring) + threadIdx.x * 16;
   float dwa[4] = {}, dwb[4] = {}, wa[4], wb[4];
   load_weight<T, D, INTER>(a.w[side], a.w_f32, l, wa, wb);
-#pragma unroll 1
-  for (int64_t u = blockIdx.x - (side ? a.ctas[0] : 0); u < tgroups * runs; u += a.ctas[side]) {
-    // runs change slowest: the CTAs work on neighbouring tokens of the same heads
-    const int64_t tok = (u % tgroups) * kGroups + grp;
-    const int run = static_cast<int>(u / tgroups);
-    const bool in = tok < ntok;
-    const int b = in ? static_cast<int>(tok / a.S) : 0, s = in ? static_cast<int>(tok % a.S) : 0;
-    const int h_begin = run * a.per_run, h_end = min(a.heads[side], h_begin + a.per_run);
-    const T* xrow = static_cast<const T*>(a.x[side].p) + b * a.x[side].sb + s * a.x[side].ss;
-    const T* grow = static_cast<const T*>(a.dy[side].p) + b * a.dy[side].sb + s * a.dy[side].ss;
-    T* drow = static_cast<T*>(a.dx[side].p) + b * a.dx[side].sb + s * a.dx[side].ss;
-    Raw<T> rx[kUnroll], rg[kUnroll], nx[kUnroll], ng[kUnroll];
-    auto load = [&](Raw<T>(&x)[kUnroll], Raw<T>(&g)[kUnroll], int h0) {
+
+  // the token and heads of a unit: runs change slowest, so that the CTAs work on neighbouring
+  // tokens of the same heads
+  auto open = [&](int u, int& b, int& s, int& h0, int& h1) -> bool {
+    const unsigned tok = static_cast<unsigned>(u % tgroups) * kGroups + grp;
+    h0 = u / tgroups * a.per_run;
+    h1 = min(heads, h0 + a.per_run);
+    const bool in = tok < static_cast<unsigned>(ntok);
+    b = in ? static_cast<int>(tok / a.S) : 0;
+    s = in ? static_cast<int>(tok % a.S) : 0;
+    return in;
+  };
+  int fu = u0;   // the unit being fetched, its next head and rows
+  int fh = 0, fh1 = 0, fstage = 0;
+  bool fin = false;
+  const T *fx = nullptr, *fg = nullptr;
+  auto fetch = [&]() {
+    if (fu < units) {
+      if (fh >= fh1) {
+        int b, s;
+        fin = open(fu, b, s, fh, fh1);
+        fx = static_cast<const T*>(a.x[side].p) + b * a.x[side].sb + s * a.x[side].ss;
+        fg = static_cast<const T*>(a.dy[side].p) + b * a.dy[side].sb + s * a.dy[side].ss;
+      }
+      const uint32_t d = slot0 + fstage * kStep;
 #pragma unroll
       for (int j = 0; j < kUnroll; ++j) {
-        x[j] = g[j] = Raw<T>{};
-        if (in && h0 + j < h_end) {
-          x[j] = load_row<T, D, INTER>(xrow + (h0 + j) * xsh, l);
-          g[j] = load_row<T, D, INTER>(grow + (h0 + j) * gsh, l);
-        }
+        const bool ok = fin && fh + j < fh1;
+        const int h = fh + j < fh1 ? fh + j : 0;  // a copy of no bytes still names a valid row
+        async_row<T, D, INTER>(d + 2 * j * kRow, fx + h * a.x[side].sh, l, ok);
+        async_row<T, D, INTER>(d + (2 * j + 1) * kRow, fg + h * a.dy[side].sh, l, ok);
       }
-    };
-    load(rx, rg, h_begin);
-    int pos = in ? checked_position(a.positions, a.pos_b, b, s, a.n_pos) : -1;
+      fh += kUnroll;
+      if (fh >= fh1) fu += a.ctas[side];
+      fstage = fstage + 1 == kBackAhead ? 0 : fstage + 1;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kBackAhead; ++i) fetch();
+
+  int stage = 0;
+#pragma unroll 1
+  for (int u = u0; u < units; u += a.ctas[side]) {
+    int b, s, h_begin, h_end;
+    const bool in = open(u, b, s, h_begin, h_end);
+    const int pos = in ? checked_position(a.positions, a.pos_b, b, s, a.n_pos) : -1;
     if (pos == -2 && l == 0) report_device_error(kStatusBadLabel, kNormSite + 2);
     const bool live = pos >= 0;
     float c[4] = {}, sn[4] = {};
     if (live) load_angles<D>(a.cos, a.sin, pos, l, c, sn);
+    T* drow = static_cast<T*>(a.dx[side].p) + b * a.dx[side].sb + s * a.dx[side].ss;
 #pragma unroll 1
     for (int h0 = h_begin; h0 < h_end; h0 += kUnroll) {
-      load(nx, ng, h0 + kUnroll);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kBackAhead - 1) : "memory");
+      Raw<T> rx[kUnroll], rg[kUnroll];
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) {
+        rx[j] = read_slot<T>(ring + threadIdx.x * 16 + stage * kStep + 2 * j * kRow);
+        rg[j] = read_slot<T>(ring + threadIdx.x * 16 + stage * kStep + (2 * j + 1) * kRow);
+      }
+      fetch();  // into the slots just read
+      stage = stage + 1 == kBackAhead ? 0 : stage + 1;
 #pragma unroll
       for (int j = 0; j < kUnroll; ++j) {
         float xa[4], xb[4], ga[4], gb[4], za[4], zb[4];
         to_pairs<T, INTER>(rx[j], xa, xb);
         to_pairs<T, INTER>(rg[j], ga, gb);
-        rx[j] = nx[j];
-        rg[j] = ng[j];
         if (!live) {  // a skipped row: zero gradients, nothing in the sums
 #pragma unroll
           for (int i = 0; i < 4; ++i) xa[i] = xb[i] = ga[i] = gb[i] = 0.f;
@@ -384,7 +461,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_rotation_back_kernel(const 
           oa[i] = r * (za[i] * wa[i] - xa[i] * k);
           ob[i] = r * (zb[i] * wb[i] - xb[i] * k);
         }
-        if (in && h0 + j < h_end) store_row<T, D, INTER>(drow + (h0 + j) * dsh, l, oa, ob);
+        if (in && h0 + j < h_end) store_row<T, D, INTER>(drow + (h0 + j) * a.dx[side].sh, l, oa, ob);
       }
     }
   }
@@ -429,7 +506,8 @@ __global__ void __launch_bounds__(1024) norm_weight_sum_kernel(const float* __re
   }
 }
 
-constexpr int kNormBackCtas = 148 * 4;
+constexpr int kNormBackCtas = 148 * 3;  // resident at once
+constexpr int kNormBackRun = 8;          // heads of a unit at most: units much smaller than a CTA's share
 
 int norm_elem_bytes(int dtype) { return dtype == BSA_F32 ? 4 : 2; }
 
@@ -452,6 +530,8 @@ int check_norm_common(const bsa_shape& s, const void* qw, const void* kw, const 
   if (s.Hq > 16384 || s.Hkv > 16384) return fail(BSA_ERR_UNSUPPORTED, "more than 16384 heads");
   if (static_cast<int64_t>(s.B) * s.Sq > INT32_MAX)
     return fail(BSA_ERR_UNSUPPORTED, "B*S exceeds 2^31 - 1");
+  if (static_cast<int64_t>(s.B) * s.Sq * std::max(s.Hq, s.Hkv) > (int64_t(1) << 36))
+    return fail(BSA_ERR_UNSUPPORTED, "more than 2^36 rows");
   if (!(eps >= 0.f)) return fail(BSA_ERR_INVALID_ARG, "eps < 0");
   if (!qw || !kw || !cos || !sin) return fail(BSA_ERR_INVALID_ARG, "null pointer");
   if (n_pos < 0) return fail(BSA_ERR_INVALID_ARG, "n_pos < 0");
@@ -497,12 +577,25 @@ int launch_norm(NormArgs& a, int dtype, int D, int interleaved, cudaStream_t st)
   return check_cuda(cudaGetLastError(), "norm_rotation_kernel");
 }
 
+template <typename T, int D>
+int launch_norm_back(const NormBackArgs& a, int ctas, int interleaved, cudaStream_t st) {
+  auto kern = interleaved ? norm_rotation_back_kernel<T, D, true> : norm_rotation_back_kernel<T, D, false>;
+  constexpr int smem = norm_back_smem<T>();
+  // the static part, 16 KB, counts too
+  const int e = check_cuda(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
+                           "cudaFuncSetAttribute(norm_rotation_back_kernel)");
+  if (e != BSA_OK) return e;
+  kern<<<ctas, kNormThreads, smem, st>>>(a);
+  count_launch();
+  return check_cuda(cudaGetLastError(), "norm_rotation_back_kernel");
+}
+
 // CTAs of the backward pass, by side in proportion to the heads: each leaves one share of its
 // side's weight sums.
 void norm_back_plan(const bsa_shape& s, int* per_run, int (&ctas)[2]) {
   const int per_cta = kNormThreads / (s.D / 8);
   const int64_t tg = (static_cast<int64_t>(s.B) * s.Sq + per_cta - 1) / per_cta;
-  *per_run = heads_per_run(tg, s.Hq + s.Hkv);
+  *per_run = std::min(kNormBackRun, heads_per_run(tg, s.Hq + s.Hkv));
   const int h[2] = {s.Hq, s.Hkv};
   for (int i = 0; i < 2; ++i) {
     const int64_t units = std::max<int64_t>(1, tg * ceil_div(h[i], *per_run));
@@ -608,18 +701,14 @@ int bsa_qk_norm_rotation_backward(bsa_heads dq_out, bsa_heads dk_out, bsa_heads 
   const int ctas = a.ctas[0] + a.ctas[1];
   cudaStream_t cs = as_stream(stream);
   if (!none) {
-#define BSA_NORM_BACK(T)                                                                        \
-  (shape.D == 64                                                                                \
-       ? (interleaved ? norm_rotation_back_kernel<T, 64, true><<<ctas, kNormThreads, 0, cs>>>(a)   \
-                      : norm_rotation_back_kernel<T, 64, false><<<ctas, kNormThreads, 0, cs>>>(a)) \
-       : (interleaved ? norm_rotation_back_kernel<T, 128, true><<<ctas, kNormThreads, 0, cs>>>(a)  \
-                      : norm_rotation_back_kernel<T, 128, false><<<ctas, kNormThreads, 0, cs>>>(a)))
-    if (shape.dtype == BSA_BF16) BSA_NORM_BACK(__nv_bfloat16);
-    else if (shape.dtype == BSA_F16) BSA_NORM_BACK(__half);
-    else BSA_NORM_BACK(float);
+#define BSA_NORM_BACK(T)                                                       \
+  (shape.D == 64 ? launch_norm_back<T, 64>(a, ctas, interleaved, cs)            \
+                 : launch_norm_back<T, 128>(a, ctas, interleaved, cs))
+    if (shape.dtype == BSA_BF16) st = BSA_NORM_BACK(__nv_bfloat16);
+    else if (shape.dtype == BSA_F16) st = BSA_NORM_BACK(__half);
+    else st = BSA_NORM_BACK(float);
 #undef BSA_NORM_BACK
-    count_launch();
-    if ((st = check_cuda(cudaGetLastError(), "norm_rotation_back_kernel")) != BSA_OK) return st;
+    if (st != BSA_OK) return st;
   }
   norm_weight_sum_kernel<<<dim3(shape.D / 32, 2), 1024, 0, cs>>>(a.part, a.ctas[0], a.ctas[1], shape.D,
                                                                   dq_weight, dk_weight);
