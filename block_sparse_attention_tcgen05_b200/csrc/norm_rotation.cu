@@ -275,16 +275,25 @@ __global__ void __launch_bounds__(kNormThreads) norm_rotation_kernel(const NormA
       float x[4], y[4];
       to_pairs<T, INTER>(cur[u], x, y);
       cur[u] = nxt[u];
-      float ss = 0.f;
+      float p0 = 0.f, p1 = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
-      const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + a.eps);
+      for (int i = 0; i < 4; i += 2) {
+        fma2(p0, p1, x[i], x[i + 1], x[i], x[i + 1], p0, p1);
+        fma2(p0, p1, y[i], y[i + 1], y[i], y[i + 1], p0, p1);
+      }
+      const float r = rsqrtf(row_sum<D>(p0 + p1) * (1.f / D) + a.eps);
       float o0[4], o1[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float ya = x[i] * r * wa[i], yb = y[i] * r * wb[i];
-        o0[i] = ya * c[i] - yb * sn[i];
-        o1[i] = ya * sn[i] + yb * c[i];
+      for (int i = 0; i < 4; i += 2) {
+        float ya0, ya1, yb0, yb1, u0, u1;
+        mul2(u0, u1, wa[i], wa[i + 1], r, r);
+        mul2(ya0, ya1, x[i], x[i + 1], u0, u1);
+        mul2(u0, u1, wb[i], wb[i + 1], r, r);
+        mul2(yb0, yb1, y[i], y[i + 1], u0, u1);
+        mul2(u0, u1, yb0, yb1, -sn[i], -sn[i + 1]);
+        fma2(o0[i], o0[i + 1], ya0, ya1, c[i], c[i + 1], u0, u1);
+        mul2(u0, u1, yb0, yb1, c[i], c[i + 1]);
+        fma2(o1[i], o1[i + 1], ya0, ya1, sn[i], sn[i + 1], u0, u1);
       }
       if (put && h0 + u < h_end) store_row<T, D, INTER>(dst + (h0 + u) * ysh, l, o0, o1);
     }
@@ -355,7 +364,7 @@ constexpr int norm_back_smem() {
 // bytes in flight cost no registers (holding one step ahead in registers ran at 71 % of the
 // HBM rate, with two CTAs of 120 registers per SM).
 template <typename T, int D, bool INTER>
-__global__ void __launch_bounds__(kNormThreads) norm_rotation_back_kernel(const NormBackArgs a) {
+__global__ void __launch_bounds__(kNormThreads, sizeof(T) == 2 ? 3 : 2) norm_rotation_back_kernel(const NormBackArgs a) {
   constexpr int L = D / 8, kGroups = kNormThreads / L;
   constexpr int kUnroll = kBackUnroll, kRow = 8 * sizeof(T) * kNormThreads, kStep = 2 * kUnroll * kRow;
   extern __shared__ __align__(16) uint8_t ring[];
@@ -441,25 +450,37 @@ __global__ void __launch_bounds__(kNormThreads) norm_rotation_back_kernel(const 
 #pragma unroll
           for (int i = 0; i < 4; ++i) xa[i] = xb[i] = ga[i] = gb[i] = 0.f;
         }
-        float ss = 0.f, dot = 0.f;
+        // pairs of fp32 operations (f32x2): the pass is close to issue-bound
+        float p0 = 0.f, p1 = 0.f, d0 = 0.f, d1 = 0.f, ta[4], tb[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          za[i] = ga[i] * c[i] + gb[i] * sn[i];
-          zb[i] = gb[i] * c[i] - ga[i] * sn[i];
-          ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
-          dot = fmaf(za[i] * wa[i], xa[i], fmaf(zb[i] * wb[i], xb[i], dot));
+        for (int i = 0; i < 4; i += 2) {
+          float u0, u1;
+          mul2(u0, u1, gb[i], gb[i + 1], sn[i], sn[i + 1]);
+          fma2(za[i], za[i + 1], ga[i], ga[i + 1], c[i], c[i + 1], u0, u1);
+          mul2(u0, u1, ga[i], ga[i + 1], -sn[i], -sn[i + 1]);
+          fma2(zb[i], zb[i + 1], gb[i], gb[i + 1], c[i], c[i + 1], u0, u1);
+          fma2(p0, p1, xa[i], xa[i + 1], xa[i], xa[i + 1], p0, p1);
+          fma2(p0, p1, xb[i], xb[i + 1], xb[i], xb[i + 1], p0, p1);
+          mul2(ta[i], ta[i + 1], za[i], za[i + 1], xa[i], xa[i + 1]);
+          mul2(tb[i], tb[i + 1], zb[i], zb[i + 1], xb[i], xb[i + 1]);
+          fma2(d0, d1, ta[i], ta[i + 1], wa[i], wa[i + 1], d0, d1);
+          fma2(d0, d1, tb[i], tb[i + 1], wb[i], wb[i + 1], d0, d1);
         }
-        ss = row_sum<D>(ss);
-        dot = row_sum<D>(dot);
+        const float ss = row_sum<D>(p0 + p1), dot = row_sum<D>(d0 + d1);
         const float r = live ? rsqrtf(ss * (1.f / D) + a.eps) : 0.f;
-        const float k = r * r * dot * (1.f / D);
+        const float nk = -(r * r * dot * (1.f / D)) * r;
         float oa[4], ob[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          dwa[i] = fmaf(za[i] * r, xa[i], dwa[i]);
-          dwb[i] = fmaf(zb[i] * r, xb[i], dwb[i]);
-          oa[i] = r * (za[i] * wa[i] - xa[i] * k);
-          ob[i] = r * (zb[i] * wb[i] - xb[i] * k);
+        for (int i = 0; i < 4; i += 2) {
+          float u0, u1;
+          fma2(dwa[i], dwa[i + 1], ta[i], ta[i + 1], r, r, dwa[i], dwa[i + 1]);
+          fma2(dwb[i], dwb[i + 1], tb[i], tb[i + 1], r, r, dwb[i], dwb[i + 1]);
+          mul2(u0, u1, wa[i], wa[i + 1], r, r);
+          mul2(oa[i], oa[i + 1], za[i], za[i + 1], u0, u1);
+          fma2(oa[i], oa[i + 1], xa[i], xa[i + 1], nk, nk, oa[i], oa[i + 1]);
+          mul2(u0, u1, wb[i], wb[i + 1], r, r);
+          mul2(ob[i], ob[i + 1], zb[i], zb[i + 1], u0, u1);
+          fma2(ob[i], ob[i + 1], xb[i], xb[i + 1], nk, nk, ob[i], ob[i + 1]);
         }
         if (in && h0 + j < h_end) store_row<T, D, INTER>(drow + (h0 + j) * a.dx[side].sh, l, oa, ob);
       }
