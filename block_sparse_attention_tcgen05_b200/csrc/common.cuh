@@ -55,6 +55,24 @@ int check_paged_cache(const bsa_paged_cache& c);
 
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
+// Launches `kern` as a programmatic dependent of the kernel before it on the stream: its CTAs
+// may become resident before that kernel has ended, and it calls wait_for_primary() before
+// it reads what that kernel wrote. Saves most of a launch's latency (about 3 us).
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 // Kernel timing hooks (bsa_profile_*): when enabled, the launch sites of the main
 // kernels record a CUDA event pair around the launch on the launch stream.
 enum ProfKernel { kProfAttention = 0, kProfScoring = 1, kProfProbe = 2, kProfCount = 3 };

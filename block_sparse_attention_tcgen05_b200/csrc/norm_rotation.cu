@@ -486,6 +486,7 @@ __global__ void __launch_bounds__(kNormThreads, sizeof(T) == 2 ? 3 : 2) norm_rot
       }
     }
   }
+  launch_dependents();
   // the lane groups' sums, added in group order
   __shared__ float red[kGroups][D];
 #pragma unroll
@@ -510,6 +511,7 @@ __global__ void __launch_bounds__(1024) norm_weight_sum_kernel(const float* __re
                                                                int nk, int D, float* __restrict__ dqw,
                                                                float* __restrict__ dkw) {
   __shared__ double red[32][33];
+  wait_for_primary();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, side = blockIdx.y;
   const int col = blockIdx.x * 32 + lane;
   const float* p = part + (side ? static_cast<size_t>(nq) * D : 0) + col;
@@ -731,10 +733,10 @@ int bsa_qk_norm_rotation_backward(bsa_heads dq_out, bsa_heads dk_out, bsa_heads 
 #undef BSA_NORM_BACK
     if (st != BSA_OK) return st;
   }
-  norm_weight_sum_kernel<<<dim3(shape.D / 32, 2), 1024, 0, cs>>>(a.part, a.ctas[0], a.ctas[1], shape.D,
-                                                                  dq_weight, dk_weight);
   count_launch();
-  return check_cuda(cudaGetLastError(), "norm_weight_sum_kernel");
+  return check_cuda(launch_dependent(norm_weight_sum_kernel, dim3(shape.D / 32, 2), dim3(1024), 0, cs, a.part,
+                                     a.ctas[0], a.ctas[1], shape.D, dq_weight, dk_weight),
+                    "norm_weight_sum_kernel");
 }
 
 int bsa_paged_qk_norm_append(bsa_heads q, bsa_heads k, bsa_heads v, int T, int Hq,

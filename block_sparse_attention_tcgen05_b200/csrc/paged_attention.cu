@@ -49,8 +49,8 @@ struct PagedArgs {
   int max_new;   // host bound of new tokens per request
   int min_rows;  // requests of at most this many rows belong to the token kernel
   float* part;
-  int splits;      // tile kernel: CTAs per tile pair over its keys
-  int units_max;   // tile kernel: bound of tile pairs per KV head
+  int tile_ctas;   // tile kernel: CTAs per KV head (a bound: those past the last one end at once)
+  int can_split;   // tile kernel: 0 when no request is long enough to be split
   int workers;     // token kernel: CTAs
   int tok_rows;    // token kernel: rows of a request that its instance holds (8 or 16)
   int one_each;    // token kernel: one CTA per (request, KV head), nothing to join
@@ -207,6 +207,7 @@ __global__ void __launch_bounds__(kTokThreads) paged_token_kernel(const PagedArg
     u_end = min(units, u_begin + span);
   }
 
+  launch_dependents();
   for (int64_t u = u_begin; u < u_end;) {
     // the (request, head) of unit u and the chunks of it that lie in this span
     int r, h, ch0, ch1, nch;
@@ -454,14 +455,22 @@ __global__ void __launch_bounds__(kTokThreads) paged_token_kernel(const PagedArg
   }
 }
 
-// Joins the partial results of one (request, KV head), one CTA each; a warp per row at a time.
+// Joins the partial results of one row of a (request, KV head): grid (requests * heads, rows).
+// The warps take the CTAs that shared the work in turn, their results are joined in order
+// through shared memory. (One warp per row walking over all of them took 31 us for the 52
+// CTAs of a 32761-key row, longer than the attention itself.)
+constexpr int kCombWarps = 8;
 template <typename T, int D>
-__global__ void __launch_bounds__(kTokThreads) token_combine_kernel(const PagedArgs a) {
-  __shared__ int s_sum[2][kTokWarps];
+__global__ void __launch_bounds__(32 * kCombWarps) token_combine_kernel(const PagedArgs a) {
+  __shared__ int s_sum[2][kCombWarps];
+  __shared__ float s_acc[kCombWarps][D];
+  __shared__ float2 s_ml[kCombWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int r = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv;
+  const int r = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv, row = blockIdx.y;
+  launch_dependents();
+  // the lengths are inputs of the call, so the place of the row is found before the wait
   int before = 0, all = 0;
-  for (int i = tid; i < a.R; i += kTokThreads) {
+  for (int i = tid; i < a.R; i += 32 * kCombWarps) {
     const int n = token_chunks(a, load_request(a, i));
     all += n;
     if (i < r) before += n;
@@ -475,43 +484,68 @@ __global__ void __launch_bounds__(kTokThreads) token_combine_kernel(const PagedA
   __syncthreads();
   before = all = 0;
 #pragma unroll
-  for (int w = 0; w < kTokWarps; ++w) {
+  for (int w = 0; w < kCombWarps; ++w) {
     before += s_sum[0][w];
     all += s_sum[1][w];
   }
   const Request q = load_request(a, r);
   const int nch = token_chunks(a, q);
-  if (nch == 0) return;
+  wait_for_primary();  // before any return: a dependent that has ended stands for its primary
+  if (nch == 0 || row >= q.n * a.G) return;
   const int64_t span = token_span(static_cast<int64_t>(all) * a.Hkv, a.workers);
   const int64_t u0 = static_cast<int64_t>(before) * a.Hkv + static_cast<int64_t>(h) * nch;
   const int w0 = static_cast<int>(u0 / span), w1 = static_cast<int>((u0 + nch - 1) / span);
   if (w0 == w1) return;  // one CTA had all of it and wrote the result
-  for (int row = warp; row < q.n * a.G; row += kTokWarps) {
-    float mt = -INFINITY;
-    for (int w = w0 + lane; w <= w1; w += 32)
-      mt = fmaxf(mt, token_slot(a, w, w == w0 ? 1 : 0, D)[kTokenRows * D + 2 * row]);
+  float mt = -INFINITY, lt = 0.f, acc[D / 32] = {};
+  for (int w = w0 + warp; w <= w1; w += 4 * kCombWarps) {
+    float2 ml[4], v[4][D / 64];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-    float lt = 0.f, acc[D / 32] = {};
-#pragma unroll 4
-    for (int w = w0; w <= w1; ++w) {
-      const float* s = token_slot(a, w, w == w0 ? 1 : 0, D);
-      const float2 ml = *reinterpret_cast<const float2*>(s + kTokenRows * D + 2 * row);
-      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mt);
-      lt = fmaf(ml.y, f, lt);
+    for (int i = 0; i < 4; ++i) {
+      const int wi = w + i * kCombWarps;
+      ml[i] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int e = 0; e < D / 64; ++e) {
-        const float2 v = *reinterpret_cast<const float2*>(s + row * D + 64 * e + 2 * lane);
-        acc[2 * e] = fmaf(v.x, f, acc[2 * e]);
-        acc[2 * e + 1] = fmaf(v.y, f, acc[2 * e + 1]);
+      for (int e = 0; e < D / 64; ++e) v[i][e] = make_float2(0.f, 0.f);
+      if (wi <= w1) {
+        const float* s = token_slot(a, wi, wi == w0 ? 1 : 0, D);
+        ml[i] = *reinterpret_cast<const float2*>(s + kTokenRows * D + 2 * row);
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) v[i][e] = *reinterpret_cast<const float2*>(s + row * D + 64 * e + 2 * lane);
       }
     }
-    const float inv = lt > 0.f ? 1.f / lt : 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (ml[i].x == -INFINITY) continue;  // saw no key of this row
+      const float mn = fmaxf(mt, ml[i].x), f0 = ex2(mt - mn), f1 = ex2(ml[i].x - mn);
+      lt = lt * f0 + ml[i].y * f1;
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e) {
+        acc[2 * e] = acc[2 * e] * f0 + v[i][e].x * f1;
+        acc[2 * e + 1] = acc[2 * e + 1] * f0 + v[i][e].y * f1;
+      }
+      mt = mn;
+    }
+  }
+  if (lane == 0) s_ml[warp] = make_float2(mt, lt);
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e)
+    *reinterpret_cast<float2*>(&s_acc[warp][64 * e + 2 * lane]) = make_float2(acc[2 * e], acc[2 * e + 1]);
+  __syncthreads();
+  if (tid < D / 2) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kCombWarps; ++w) m = fmaxf(m, s_ml[w].x);
+    float l = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < kCombWarps; ++w) {
+      const float f = s_ml[w].x == -INFINITY ? 0.f : ex2(s_ml[w].x - m);
+      l = fmaf(s_ml[w].y, f, l);
+      o0 = fmaf(s_acc[w][2 * tid], f, o0);
+      o1 = fmaf(s_acc[w][2 * tid + 1], f, o1);
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
     T* po = static_cast<T*>(a.out) + (static_cast<int64_t>(h) * a.G + row % a.G) * a.oh +
             static_cast<int64_t>(q.t0 + row / a.G) * a.ot;
-#pragma unroll
-    for (int e = 0; e < D / 64; ++e)
-      *reinterpret_cast<uint32_t*>(po + 64 * e + 2 * lane) = pack_pair<T>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    *reinterpret_cast<uint32_t*>(po + 2 * tid) = pack_pair<T>(o0 * inv, o1 * inv);
   }
 }
 
@@ -546,43 +580,115 @@ enum {
   TB_INFO = TB_KV_EMPTY + kTileStages,
   TB_Q = TB_INFO + kTileInfo,
   TB_S,            // two: logits of a tile ready
-  TB_P = TB_S + 2,  // two: weights of a tile written
-  TB_O = TB_P + 2,  // two: output of a tile final
+  TB_P = TB_S + 2,  // four: weights of a tile's keys 0..63 and 64..127 written
+  TB_O = TB_P + 4,  // two: output of a tile final
   TB_DRAIN = TB_O + 2,
   TB_COUNT
 };
 
-// Tile pair u of a KV head: its request and its index there (false past the last one). The
-// requests' pairs are counted by one warp, 32 requests at a time.
-__device__ __forceinline__ bool find_tile(const PagedArgs& a, int u, int lane, int* r_out, int* tile_out) {
-  int base = 0;
-  for (int r0 = 0; r0 < a.R; r0 += 32) {
-    const int r = r0 + lane;
-    int n = 0;
-    if (r < a.R) {
-      const int64_t rows = static_cast<int64_t>(load_request(a, r).n) * a.G;
-      n = rows > a.min_rows ? static_cast<int>((rows + kTileRows - 1) / kTileRows) : 0;
+// How the tile kernel's work is cut. A request's rows make tile pairs of 256 rows, and a pair's
+// keys are split over CTAs so that none has many more than `quantum` chunks of 128 keys. With
+// `share` the chunks of one SM if the whole call's were spread evenly: half the share where it is
+// long (32 chunks, some 60 us), so that long requests are split among short ones and the last
+// CTA ends little after the others; the share itself where it is short, so that one wave does
+// it all; and at least kTileMinChunks, since a CTA costs about as much as 4 chunks to start and
+// end. With many more pairs than SMs none is split. All of it follows from the lengths,
+// which live on the GPU, so each CTA works it out.
+constexpr int kTileSms = 148;
+constexpr int kTileJobs = 2 * kTileSms;  // the quantum is never below the work over this
+constexpr int kTileLongShare = 32;
+constexpr int kTileMinChunks = 8;
+
+struct TileJob {
+  int r, tile, split, splits;
+  int slot;  // of the partial results, when splits > 1: slot + split
+};
+
+__device__ __forceinline__ int tile_pairs(const PagedArgs& a, const Request& q) {
+  const int64_t rows = static_cast<int64_t>(q.n) * a.G;
+  return rows > a.min_rows ? static_cast<int>((rows + kTileRows - 1) / kTileRows) : 0;
+}
+__device__ __forceinline__ int tile_chunks(const Request& q) { return (q.len + 127) >> 7; }
+
+__device__ __forceinline__ int64_t tile_quantum(const PagedArgs& a, int64_t work) {
+  const int64_t all = work * a.Hkv, share = (all + kTileSms - 1) / kTileSms;
+  if (share >= kTileLongShare) return (all + kTileJobs - 1) / kTileJobs;
+  return share < kTileMinChunks ? kTileMinChunks : share;
+}
+// Up to a quarter more than the quantum is not split.
+__device__ __forceinline__ int tile_splits(int chunks, int64_t quantum) {
+  return 4 * static_cast<int64_t>(chunks) <= 5 * quantum ? 1 : static_cast<int>((chunks + quantum - 1) / quantum);
+}
+
+// Job u of a KV head (by one warp, 32 requests at a time); with kJoin, the u-th pair that is
+// split. False past the last one.
+template <bool kJoin>
+__device__ __forceinline__ bool find_tile(const PagedArgs& a, int u, int lane, TileJob* job) {
+  int pairs = 0, chunks = 0;  // of the lane's request of a round
+  auto look = [&](int r0) {
+    pairs = chunks = 0;
+    if (r0 + lane < a.R) {
+      const Request q = load_request(a, r0 + lane);
+      pairs = tile_pairs(a, q);
+      chunks = tile_chunks(q);
     }
-    int incl = n;
+  };
+  look(0);
+  int64_t quantum = INT32_MAX;
+  if (a.can_split) {
+    int64_t work = static_cast<int64_t>(pairs) * chunks;
+    if (a.R > 32) {
+      for (int r0 = 32; r0 < a.R; r0 += 32) {
+        look(r0);
+        work += static_cast<int64_t>(pairs) * chunks;
+      }
+      look(0);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+    quantum = tile_quantum(a, work);
+  }
+  int base = 0, slots = 0;
+  for (int r0 = 0; r0 < a.R; r0 += 32) {
+    if (r0 > 0) look(r0);
+    const int ns = tile_splits(chunks, quantum);
+    const int n = kJoin ? (ns > 1 ? pairs : 0) : pairs * ns;  // this lane's jobs
+    const int p = ns > 1 ? pairs * ns : 0;                    // and partial results
+    int incl = n, pincl = p;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+      const int y = __shfl_up_sync(0xffffffffu, incl, o), z = __shfl_up_sync(0xffffffffu, pincl, o);
+      if (lane >= o) {
+        incl += y;
+        pincl += z;
+      }
     }
     const unsigned hit = __ballot_sync(0xffffffffu, base + incl > u);
     if (hit) {
       const int src = __ffs(hit) - 1;
-      *r_out = r0 + src;
-      *tile_out = u - base - __shfl_sync(0xffffffffu, incl - n, src);
+      const int k = u - base - __shfl_sync(0xffffffffu, incl - n, src);
+      job->r = r0 + src;
+      job->splits = __shfl_sync(0xffffffffu, ns, src);
+      job->tile = kJoin ? k : k / job->splits;
+      job->split = kJoin ? 0 : k % job->splits;
+      job->slot = slots + __shfl_sync(0xffffffffu, pincl - p, src) + job->tile * job->splits;
       return true;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
+    slots += __shfl_sync(0xffffffffu, pincl, 31);
   }
   return false;
 }
 
-__device__ __forceinline__ size_t tile_part_row(const PagedArgs& a, int u, int h, int split, int row) {
-  return ((static_cast<size_t>(u) * a.Hkv + h) * a.splits + split) * kTileRows + row;
+// A pair is split only if it has more chunks than the quantum, which is at least the work over
+// kTileJobs: the pairs that are split have at most 2 kTileJobs parts between them, over all heads.
+constexpr int kTileSlots = 2 * kTileJobs;
+
+__device__ __forceinline__ size_t tile_part_row(const PagedArgs& a, int slot, int h, int row) {
+  return (static_cast<size_t>(slot) * a.Hkv + h) * kTileRows + row;
+}
+__device__ __forceinline__ float* tile_part_ml(const PagedArgs& a, int D) {
+  return a.part + static_cast<size_t>(kTileSlots) * kTileRows * D;
 }
 
 template <typename T, int D>
@@ -602,29 +708,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ids + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* never = reinterpret_cast<int*>(tmem_slot + 2);
-  int* where = reinterpret_cast<int*>(tmem_slot + 3);  // request, tile (or -1)
+  TileJob* where = reinterpret_cast<TileJob*>(tmem_slot + 3);  // r < 0: none
   const uint32_t bar0 = smem_u32(bars);
 #define TBAR(i) (bar0 + 8u * static_cast<uint32_t>(i))
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int split = blockIdx.x % a.splits;
-  // causal tiles near the end of a request see the most keys: they start first
-  const int u = a.units_max - 1 - static_cast<int>(blockIdx.x / a.splits);
   const int h = blockIdx.y;
 
   if (warp == 0) {
-    int r = 0, tile = 0;
-    const bool found = find_tile(a, u, lane, &r, &tile);
+    TileJob job{};
+    // causal tiles near the end of a request see the most keys: they start first
+    const bool found = find_tile<false>(a, a.tile_ctas - 1 - static_cast<int>(blockIdx.x), lane, &job);
     if (lane == 0) {
-      where[0] = found ? r : -1;
-      where[1] = tile;
+      if (!found) job.r = -1;
+      *where = job;
     }
     if (blockIdx.x == 0 && blockIdx.y == 0)
       for (int i = lane; i < a.R; i += 32) check_request(a, i);
   } else if (warp == 1) {
     if (lane == 0) {
       for (int i = 0; i < TB_COUNT; ++i)
-        mbar_init(TBAR(i), i == TB_Q ? 256u : (i == TB_P || i == TB_P + 1 ? 128u : 1u));
+        mbar_init(TBAR(i), i == TB_Q ? 8u : (i >= TB_P && i < TB_P + 4 ? 4u : 1u));  // by warp
       *abort_flag = 0;
       *never = 0;
       fence_mbarrier_init();
@@ -632,31 +736,34 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       prefetch_tmap(&tmV);
     }
   }
-  __syncthreads();
-  const int r = where[0];
-  if (r < 0) return;  // no such tile: the same for the whole CTA
   if (warp == 2) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int r = where->r;
+  launch_dependents();
+  if (r < 0) {  // no such job: the same for the whole CTA
+    if (warp == 2) tmem_dealloc(tmem, 512);
+    wait_for_primary();
+    return;
+  }
   const Request q = load_request(a, r);
-  const int row0 = where[1] * kTileRows;
+  const int row0 = where->tile * kTileRows, split = where->split, splits = where->splits;
   const int rows = min(kTileRows, q.n * a.G - row0);  // > 0
   const bool two = rows > 128;
   // keys that the CTA's last row sees, and this split's share of them in 128-key steps
   const int last_tok = (row0 + rows - 1) / a.G;
   const int key_end = a.causal ? min(q.len, q.ctx + last_tok + 1) : q.len;
   const int steps = (key_end + 127) >> 7;
-  const int key_lo = static_cast<int>(static_cast<int64_t>(steps) * split / a.splits) << 7;
-  const int key_hi = min(key_end, static_cast<int>(static_cast<int64_t>(steps) * (split + 1) / a.splits) << 7);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-
+  const int key_lo = static_cast<int>(static_cast<int64_t>(steps) * split / splits) << 7;
+  const int key_hi = min(key_end, static_cast<int>(static_cast<int64_t>(steps) * (split + 1) / splits) << 7);
   // a warp waits as one: what follows a wait is warp-wide
   auto wait_all = [&](uint32_t bar, uint32_t parity, int site) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, site));
+    return __all_sync(0xffffffffu, mbar_wait_poll(bar, parity, abort_flag, site));
   };
   if (warp == 9) {
     // ------------------------------------------------ TMA warp: gathers chunks page by page
@@ -664,43 +771,48 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int lu_shift = min(a.page_shift, 7), lu = 1 << lu_shift, per_chunk = 128 >> lu_shift;
     const int32_t* trow = a.table + r * a.table_stride;
     const uint8_t* mrow = a.mask ? a.mask + r * a.mr + h * a.mg : nullptr;
-    int cursor = key_lo >> lu_shift;
-    const int cursor_end = (key_hi + lu - 1) >> lu_shift;
+    const int end = (key_hi + lu - 1) >> lu_shift;
+    // Lane i looks at load base + i of the request (its page, -1 where it is masked or behind the
+    // end); the next 32 are looked up while these are used.
+    auto look = [&](int base) -> int {
+      const int i = base + lane;
+      if (i >= end) return -1;
+      const int pg = static_cast<int>((static_cast<int64_t>(i) << lu_shift) >> a.page_shift);
+      const int id = trow[pg];
+      if (mrow && !mrow[pg]) return -1;
+      if (id < 0 || id >= a.n_pages) {
+        report_device_error(kStatusBadLabel, kPagedSite + 1);
+        return -1;
+      }
+      return id;
+    };
+    int base = key_lo >> lu_shift;
+    int id = look(base), id_next = look(base + 32);
+    unsigned left = __ballot_sync(0xffffffffu, id >= 0);
     uint32_t loads = 0;  // stages filled so far
     bool ok = true;
     for (int j = 0; ok; ++j) {
+      // (the record is free: the stage of the last chunk's keys was last used by the values of
+      // chunk j - 4, whose product waited for the softmax of that chunk)
       TileInfo* ti = info + j % kTileInfo;
       int filled = 0, last_i = -1;
-      // the record is free: the stage of this chunk's keys was last used by the values of
-      // chunk j - 3, whose product waited for the softmax of that chunk
-      if (loads >= kTileStages)
-        ok = wait_all(TBAR(TB_KV_EMPTY + loads % kTileStages), ((loads / kTileStages) - 1) & 1, kPagedSite + 10);
-      if (!ok) break;
-      while (filled < per_chunk && cursor < cursor_end) {
-        const int i = cursor + lane;
-        int id = -1;
-        if (i < cursor_end) {
-          const int pg = static_cast<int>((static_cast<int64_t>(i) << lu_shift) >> a.page_shift);
-          if (!mrow || mrow[pg]) {
-            id = trow[pg];
-            if (id < 0 || id >= a.n_pages) {
-              report_device_error(kStatusBadLabel, kPagedSite + 1);
-              id = -1;
-            }
-          }
-        }
-        const unsigned kept = __ballot_sync(0xffffffffu, id >= 0);
-        const int rank = filled + __popc(kept & ((1u << lane) - 1u));
-        const bool take = id >= 0 && rank < per_chunk;
+      while (filled < per_chunk && base < end) {
+        const int rank = filled + __popc(left & ((1u << lane) - 1u));
+        const bool take = ((left >> lane) & 1u) && rank < per_chunk;
         if (take) {
           ids[rank] = id;
-          for (int gk = 0; gk < lu / 16; ++gk) ti->pos[rank * (lu / 16) + gk] = (i << lu_shift) + 16 * gk;
+          for (int gk = 0; gk < lu / 16; ++gk) ti->pos[rank * (lu / 16) + gk] = ((base + lane) << lu_shift) + 16 * gk;
         }
         const unsigned taken = __ballot_sync(0xffffffffu, take);
-        const int n = __popc(taken);
-        filled += n;
-        if (n) last_i = cursor + 31 - __clz(taken);
-        cursor += filled == per_chunk ? (32 - __clz(taken)) : 32;
+        filled += __popc(taken);
+        if (taken) last_i = base + 31 - __clz(taken);
+        left &= ~taken;
+        if (left == 0) {
+          base += 32;
+          id = id_next;
+          id_next = look(base + 32);
+          left = __ballot_sync(0xffffffffu, id >= 0);
+        }
       }
       const int granules = filled * (lu / 16);
       if (lane < 8 && lane >= granules) ti->pos[lane] = kAbsent;
@@ -718,8 +830,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
         const uint32_t stage = loads % kTileStages;
-        if (kv == 1 && loads >= kTileStages) {
-          ok = wait_all(TBAR(TB_KV_EMPTY + stage), ((loads / kTileStages) - 1) & 1, kPagedSite + 11);
+        if (loads >= kTileStages) {
+          ok = __all_sync(0xffffffffu, mbar_wait_poll(TBAR(TB_KV_EMPTY + stage), ((loads / kTileStages) - 1) & 1,
+                                                 abort_flag, kPagedSite + 11));
           if (!ok) break;
         }
         if (lane == 0) mbar_arrive_expect_tx(TBAR(TB_KV_FULL + stage), filled * lu * D * 2);
@@ -737,7 +850,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     // every copy has landed before the CTA may end
     for (uint32_t i = loads > kTileStages ? loads - kTileStages : 0; i < loads; ++i)
-      mbar_wait(TBAR(TB_KV_FULL + i % kTileStages), (i / kTileStages) & 1, never, kPagedSite + 12);
+      mbar_wait_poll(TBAR(TB_KV_FULL + i % kTileStages), (i / kTileStages) & 1, never, kPagedSite + 12);
   } else if (warp == 8) {
     // ------------------------------------------------ MMA warp
     // Tile t's logits and, over them, its weights live in TMEM columns 128 t .., its output in
@@ -763,13 +876,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       __syncwarp();
     };
-    auto issue_pv = [&](int t, uint32_t stage, bool first) {
+    auto issue_pv = [&](int t, int half, uint32_t stage, bool first) {
       if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
+        for (int k4 = 0; k4 < 4; ++k4) {
+          const int kk = 4 * half + k4;
           mma_ts<false>(tmem + 256 + 128 * t, tmem + 128 * t + kk * 8,
                         dV + static_cast<uint64_t>((stage * Cfg::TILE + kk * 2048) >> 4), kIdPV,
                         (!first || kk > 0) ? 1u : 0u);
+        }
       }
       __syncwarp();
     };
@@ -806,9 +921,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!(ok = wait_all(TBAR(TB_INFO + (j + 1) % kTileInfo), ((j + 1) / kTileInfo) & 1, kPagedSite + 24))) break;
       const int next_rows = info[(j + 1) % kTileInfo].rows;
       for (int t = 0; ok && t < (two ? 2 : 1); ++t) {
-        if (!(ok = wait_all(TBAR(TB_P + t), j & 1, kPagedSite + 25))) break;
+        if (!(ok = wait_all(TBAR(TB_P + 2 * t), j & 1, kPagedSite + 25))) break;
         tc_fence_after();
-        issue_pv(t, vst, j == 0);
+        issue_pv(t, 0, vst, j == 0);
+        if (!(ok = wait_all(TBAR(TB_P + 2 * t + 1), j & 1, kPagedSite + 28))) break;
+        tc_fence_after();
+        issue_pv(t, 1, vst, j == 0);
         if (t == (two ? 1 : 0)) commit(TBAR(TB_KV_EMPTY + vst));
         if (next_rows > 0) {
           if (t == 0 && !(ok = wait_all(TBAR(TB_KV_FULL + kst), kph, kPagedSite + 26))) break;
@@ -824,23 +942,39 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     // every product has completed before the CTA may end
     commit(TBAR(TB_DRAIN));
-    mbar_wait(TBAR(TB_DRAIN), 0, never, kPagedSite + 27);
+    mbar_wait_poll(TBAR(TB_DRAIN), 0, never, kPagedSite + 27);
   } else {
     // ------------------------------------------------ softmax: one thread per row
     const int t = warp >> 2, rr = tid & 127;
     const int row = row0 + 128 * t + rr;
     const bool live = 128 * t + rr < rows;
     const int tok = row / a.G, hq = h * a.G + row % a.G;
-    // this row of Q into the swizzled tile (16-byte piece p of row rr at p ^ (rr & 7))
+    // Rows of a warp move whole, UN lanes of 16 bytes to a row: with a lane per row every access
+    // touched 32 lines, 4000 cycles of Q and 8000 of partial results for a CTA.
+    constexpr int UN = D / 8;
+    const int u = lane % UN;
+    auto row_of = [&](int i) { return i * (32 / UN) + lane / UN; };  // of the warp's 32
+    auto other_row = [&](const void* p, int r) {
+      return reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(p), r));
+    };
+    // this warp's rows of Q into the swizzled tile (16-byte piece u of row r at u ^ (r & 7))
     {
       const T* src = static_cast<const T*>(a.q) + hq * a.qh + static_cast<int64_t>(q.t0 + tok) * a.qt;
+      uint4 v[UN];
 #pragma unroll
-      for (int p = 0; p < D / 8; ++p) {
-        const uint4 v = live ? *reinterpret_cast<const uint4*>(src + 8 * p) : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(smem + t * Cfg::TILE + (p >> 3) * 16384 + rr * 128 + (((p & 7) ^ (rr & 7)) << 4)) = v;
+      for (int i = 0; i < UN; ++i) {
+        const int r = row_of(i);
+        const uint8_t* p = other_row(src, r) + 16 * u;
+        v[i] = 128 * t + (warp & 3) * 32 + r < rows ? ldg_stream(p) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < UN; ++i) {
+        const int r = (warp & 3) * 32 + row_of(i);
+        *reinterpret_cast<uint4*>(smem + t * Cfg::TILE + (u >> 3) * 16384 + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = v[i];
       }
       fence_proxy_async_smem();
-      mbar_arrive(TBAR(TB_Q));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(TBAR(TB_Q));
     }
     const int lim = live ? (a.causal ? min(q.len - 1, q.ctx + tok) : q.len - 1) : -1;
     // the smallest reach of the tile's rows (its first row's): chunks up to it need no mask
@@ -915,47 +1049,72 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           w[c] = pack_pair<T>(x0, x1);
         }
         tmem_st16(tS + 16 * i, w);
+        if (i & 1) {  // half of the keys: their product may start
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(TBAR(TB_P + 2 * t + (i >> 1)));
+        }
       }
       l_run += (sa0 + sa1) + (sb0 + sb1);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(TBAR(TB_P + t));
     }
     if (ok && nch > 0) ok = wait_all(TBAR(TB_O + t), 0, kPagedSite + 32);
     if (ok && (t == 0 || two)) {
       tc_fence_after();
+      // out through the tile's Q, which no product reads any more: each lane's row (in 16-byte
+      // pieces, piece u of row r at u ^ r), then row by row
       const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-      T* po = static_cast<T*>(a.out) + hq * a.oh + static_cast<int64_t>(q.t0 + tok) * a.ot;
-      const size_t prow = a.splits > 1 ? tile_part_row(a, u, h, split, 128 * t + rr) : 0;
-      const size_t all_rows = static_cast<size_t>(a.units_max) * a.Hkv * a.splits * kTileRows;
-#pragma unroll 1
-      for (int p = 0; p < D / 32; ++p) {
-        float o[32];
+      uint8_t* stage = smem + t * Cfg::TILE + (warp & 3) * (Cfg::TILE / 4);
+      const size_t prow = splits > 1 ? tile_part_row(a, where->slot + split, h, 128 * t + rr) : 0;
+      auto put = [&](int piece, const uint4& x) {
+        *reinterpret_cast<uint4*>(stage + lane * (2 * D) + ((piece ^ (lane & (UN - 1))) << 4)) = x;
+      };
+      auto drain = [&](void* row_ptr) {
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < UN; ++i) {
+          const int r = row_of(i);
+          uint8_t* p = other_row(row_ptr, r);
+          const uint4 x = *reinterpret_cast<const uint4*>(stage + r * (2 * D) + ((u ^ (r & (UN - 1))) << 4));
+          if (128 * t + (warp & 3) * 32 + r < rows) *reinterpret_cast<uint4*>(p + 16 * u) = x;
+        }
+        __syncwarp();
+      };
+      auto take = [&](int col, float(&o)[32]) {
         if (nch > 0) {
-          tmem_ld32(tO + p * 32, o);
+          tmem_ld32(tO + col, o);
           tmem_wait_ld();
         } else {
 #pragma unroll
           for (int c = 0; c < 32; ++c) o[c] = 0.f;
         }
-        if (live && a.splits > 1) {
+      };
+      if (splits > 1) {  // unnormalised fp32, half of the columns at a time
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            *reinterpret_cast<float4*>(a.part + prow * D + p * 32 + 4 * c) =
-                make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-        } else if (live) {
+          for (int p = 0; p < D / 64; ++p) {
+            float o[32];
+            take(half * (D / 2) + p * 32, o);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) put(8 * p + c, *reinterpret_cast<uint4*>(o + 4 * c));
+          }
+          drain(a.part + prow * D + half * (D / 2));
+        }
+      } else {
+#pragma unroll
+        for (int p = 0; p < D / 32; ++p) {
+          float o[32];
+          take(p * 32, o);
           uint32_t w[16];
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
-            w[c] = l_run > 0.f ? pack_pair<T>(o[2 * c] * inv, o[2 * c + 1] * inv) : 0u;
+          for (int c = 0; c < 16; ++c) w[c] = l_run > 0.f ? pack_pair<T>(o[2 * c] * inv, o[2 * c + 1] * inv) : 0u;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<uint4*>(po + p * 32 + 8 * c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+          for (int c = 0; c < 4; ++c) put(4 * p + c, make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]));
         }
-        __syncwarp();
+        drain(static_cast<T*>(a.out) + hq * a.oh + static_cast<int64_t>(q.t0 + tok) * a.ot);
       }
-      if (live && a.splits > 1)
-        *reinterpret_cast<float2*>(a.part + all_rows * D + prow * 2) = make_float2(m_run, l_run);
+      if (live && splits > 1) *reinterpret_cast<float2*>(tile_part_ml(a, D) + prow * 2) = make_float2(m_run, l_run);
     }
   }
 #undef TBAR
@@ -965,42 +1124,74 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  // what follows on the stream waits for this kernel alone: it ends after the one before it
+  wait_for_primary();
 }
 
-// Joins the key splits of a tile pair: grid (units, Hkv, 8 row groups), a warp per row.
+// Joins the parts of the pairs that are split: grid (pairs * heads, row groups), four rows (of
+// 128 values; eight of 64) per warp at a time, four parts of each on their way at once.
+constexpr int kJoinThreads = 256;
+template <int D>
+constexpr int tile_join_rows() { return kJoinThreads / 32 * 4 * (128 / D); }  // rows of a CTA
 template <typename T, int D>
-__global__ void __launch_bounds__(256) tile_combine_kernel(const PagedArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) tile_combine_kernel(const PagedArgs a) {
+  constexpr int L = D / 4;  // lanes of a row
+  constexpr int kRows = 4;  // rows of a lane group
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int r = 0, tile = 0;
-  const int u = blockIdx.x, h = blockIdx.y;
-  if (!find_tile(a, u, lane, &r, &tile)) return;
-  const Request q = load_request(a, r);
-  const int rows = min(kTileRows, q.n * a.G - tile * kTileRows);
-  const float* ml = a.part + static_cast<size_t>(a.units_max) * a.Hkv * a.splits * kTileRows * D;
-  for (int rr = blockIdx.z * 8 + warp; rr < rows; rr += 64) {
-    float mt = -INFINITY;
-    for (int s = 0; s < a.splits; ++s) mt = fmaxf(mt, ml[2 * tile_part_row(a, u, h, s, rr)]);
-    float lt = 0.f, acc[D / 32] = {};
-    for (int s = 0; s < a.splits; ++s) {
-      const size_t prow = tile_part_row(a, u, h, s, rr);
-      const float2 x = *reinterpret_cast<const float2*>(ml + 2 * prow);
-      if (x.y <= 0.f) continue;  // a split that saw no key of this row
-      const float f = ex2(x.x - mt);
-      lt = fmaf(x.y, f, lt);
+  const int h = blockIdx.x % a.Hkv, l = lane % L;
+  TileJob job{};
+  const bool found = find_tile<true>(a, blockIdx.x / a.Hkv, lane, &job);
+  wait_for_primary();  // before any return: a dependent that has ended stands for its primary
+  if (!found) return;
+  const Request q = load_request(a, job.r);
+  const int rows = min(kTileRows, q.n * a.G - job.tile * kTileRows);
+  const float* ml = tile_part_ml(a, D);
+  const int rr0 = (blockIdx.y * (kJoinThreads / 32) + warp) * kRows * (32 / L) + lane / L;
+  float m[kRows], sum[kRows];
+  float4 acc[kRows];
 #pragma unroll
-      for (int e = 0; e < D / 64; ++e) {
-        const float2 o = *reinterpret_cast<const float2*>(a.part + prow * D + 64 * e + 2 * lane);
-        acc[2 * e] = fmaf(o.x, f, acc[2 * e]);
-        acc[2 * e + 1] = fmaf(o.y, f, acc[2 * e + 1]);
+  for (int i = 0; i < kRows; ++i) {
+    m[i] = -INFINITY;
+    sum[i] = 0.f;
+    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll 2
+  for (int s = 0; s < job.splits; ++s) {
+    float2 x[kRows];
+    float4 o[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int rr = rr0 + i * (32 / L);
+      x[i] = make_float2(-INFINITY, 0.f);
+      o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (rr < rows) {
+        const size_t prow = tile_part_row(a, job.slot + s, h, rr);
+        x[i] = *reinterpret_cast<const float2*>(ml + 2 * prow);
+        o[i] = *reinterpret_cast<const float4*>(a.part + prow * D + 4 * l);
       }
     }
-    const float inv = lt > 0.f ? 1.f / lt : 0.f;
-    const int row = tile * kTileRows + rr;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      if (x[i].x == -INFINITY) continue;  // a part that saw no key of this row
+      const float mn = fmaxf(m[i], x[i].x), f0 = ex2(m[i] - mn), f1 = ex2(x[i].x - mn);
+      sum[i] = sum[i] * f0 + x[i].y * f1;
+      acc[i].x = acc[i].x * f0 + o[i].x * f1;
+      acc[i].y = acc[i].y * f0 + o[i].y * f1;
+      acc[i].z = acc[i].z * f0 + o[i].z * f1;
+      acc[i].w = acc[i].w * f0 + o[i].w * f1;
+      m[i] = mn;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int rr = rr0 + i * (32 / L);
+    if (rr >= rows) continue;
+    const float inv = sum[i] > 0.f ? 1.f / sum[i] : 0.f;
+    const int row = job.tile * kTileRows + rr;
     T* po = static_cast<T*>(a.out) + (static_cast<int64_t>(h) * a.G + row % a.G) * a.oh +
             static_cast<int64_t>(q.t0 + row / a.G) * a.ot;
-#pragma unroll
-    for (int e = 0; e < D / 64; ++e)
-      *reinterpret_cast<uint32_t*>(po + 64 * e + 2 * lane) = pack_pair<T>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    *reinterpret_cast<uint2*>(po + 4 * l) =
+        make_uint2(pack_pair<T>(acc[i].x * inv, acc[i].y * inv), pack_pair<T>(acc[i].z * inv, acc[i].w * inv));
   }
 }
 
@@ -1009,7 +1200,7 @@ struct PagedPlan {
   bool token, tile;  // which kernels run
   int min_rows;      // rows up to which a request is the token kernel's
   int workers, one_each;
-  int units_max, splits;
+  int tile_ctas, can_split;
   size_t bytes;
   size_t tile_off;
 };
@@ -1030,15 +1221,13 @@ PagedPlan paged_plan(int R, int T, int Hq, int Hkv, int D, int max_new, int widt
   if (p.token && !p.one_each)
     b = align_up(static_cast<size_t>(p.workers) * 2 * kTokenRows * (D + 2) * sizeof(float), 256);
   p.tile_off = b;
-  p.splits = 1;
   if (p.tile) {
-    // a request's tiles: at most its rows / 256 rounded up; the sum over requests is at most
-    p.units_max = static_cast<int>(static_cast<int64_t>(T) * G / kTileRows + std::min(R, T));
-    const int64_t ctas = static_cast<int64_t>(p.units_max) * Hkv;
-    const int64_t most_splits = std::max<int64_t>(1, std::min<int64_t>(16, keys / 1024));
-    if (ctas < 148) p.splits = static_cast<int>(std::min<int64_t>(most_splits, 148 / ctas));
-    if (p.splits > 1)
-      b += align_up(static_cast<size_t>(ctas) * p.splits * kTileRows * (D + 2) * sizeof(float), 256);
+    // a request's pairs: at most its rows / 256, rounded up; splitting adds at most the work over
+    // the quantum, which is at least the work over kTileJobs
+    const int64_t pairs = static_cast<int64_t>(T) * G / kTileRows + std::min(R, T);
+    p.can_split = keys > kTileMinChunks * 128;
+    p.tile_ctas = static_cast<int>(pairs + (p.can_split ? ceil_div(kTileJobs, Hkv) : 0));
+    if (p.can_split) b += align_up(static_cast<size_t>(kTileSlots) * kTileRows * (D + 2) * sizeof(float), 256);
   }
   p.bytes = std::max<size_t>(b, 256);
   return p;
@@ -1077,19 +1266,22 @@ int launch_paged(PagedArgs a, const PagedPlan& p, const bsa_paged_cache& c, char
     }
     kern<<<p.workers, kTokThreads, smem, st>>>(t);
     count_launch();
+    int e = check_cuda(cudaGetLastError(), "paged_token_kernel");
+    if (e != BSA_OK) return e;
     if (!p.one_each) {
-      token_combine_kernel<T, D><<<a.R * a.Hkv, kTokThreads, 0, st>>>(t);
+      e = check_cuda(launch_dependent(token_combine_kernel<T, D>,
+                                      dim3(a.R * a.Hkv, static_cast<unsigned>(std::min<int64_t>(most, kTokenRows))),
+                                      dim3(32 * kCombWarps), 0, st, t), "token_combine_kernel");
+      if (e != BSA_OK) return e;
       count_launch();
     }
-    const int e = check_cuda(cudaGetLastError(), "paged_token_kernel");
-    if (e != BSA_OK) return e;
   }
   if (p.tile) {
     PagedArgs t = a;
     t.part = reinterpret_cast<float*>(ws + p.tile_off);
     t.min_rows = p.min_rows;
-    t.splits = p.splits;
-    t.units_max = p.units_max;
+    t.tile_ctas = p.tile_ctas;
+    t.can_split = p.can_split;
     CUtensorMap mk, mv;
     const CUtensorMapDataType dt = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -1107,14 +1299,24 @@ int launch_paged(PagedArgs a, const PagedPlan& p, const bsa_paged_cache& c, char
     e = check_cuda(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         TileCfg<D>::SMEM_LAUNCH), "cudaFuncSetAttribute(paged_tile_kernel)");
     if (e != BSA_OK) return e;
-    kern<<<dim3(p.units_max * p.splits, a.Hkv), kTileThreads, TileCfg<D>::SMEM_LAUNCH, st>>>(mk, mv, t);
+    const dim3 grid(p.tile_ctas, a.Hkv);
+    // After the token kernel's join it starts at once: it shares neither rows nor workspace with it.
+    if (p.token) {
+      e = check_cuda(launch_dependent(kern, grid, dim3(kTileThreads), TileCfg<D>::SMEM_LAUNCH, st, mk, mv, t),
+                     "paged_tile_kernel");
+    } else {
+      kern<<<grid, kTileThreads, TileCfg<D>::SMEM_LAUNCH, st>>>(mk, mv, t);
+      e = check_cuda(cudaGetLastError(), "paged_tile_kernel");
+    }
+    if (e != BSA_OK) return e;
     count_launch();
-    if (p.splits > 1) {
-      tile_combine_kernel<T, D><<<dim3(p.units_max, a.Hkv, 8), 256, 0, st>>>(t);
+    if (p.can_split) {
+      e = check_cuda(launch_dependent(tile_combine_kernel<T, D>,
+                                      dim3(ceil_div(kTileJobs, a.Hkv) * a.Hkv, kTileRows / tile_join_rows<D>()),
+                                      dim3(kJoinThreads), 0, st, t), "tile_combine_kernel");
+      if (e != BSA_OK) return e;
       count_launch();
     }
-    e = check_cuda(cudaGetLastError(), "paged_tile_kernel");
-    if (e != BSA_OK) return e;
   }
   return BSA_OK;
 }
