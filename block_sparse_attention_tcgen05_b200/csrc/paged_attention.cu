@@ -553,7 +553,10 @@ __global__ void __launch_bounds__(32 * kCombWarps) token_combine_kernel(const Pa
 constexpr int kTileRows = 256;   // rows of a CTA: two 128-row tiles
 constexpr int kTileStages = 5;   // K/V stages of 128 rows
 constexpr int kTileInfo = 4;     // chunk records in flight
-constexpr int kTileThreads = 320;  // 8 softmax warps, one MMA warp, one TMA warp
+constexpr int kTileThreads = 640;  // 16 softmax warps, two MMA warps, one TMA warp, one that waits for it
+// Registers: the launch gives every thread 96 (65536 / 640, in steps of 8); the softmax
+// warpgroups take 104 each, the last one keeps 64: 512 * 104 + 128 * 64 = 640 * 96.
+constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
 
 // A chunk's record: the key position of each of its eight 16-key granules (kAbsent where the
 // chunk holds none), the rows of it that hold keys, and the last position in it (kAbsent when
@@ -568,8 +571,8 @@ template <int D>
 struct TileCfg {
   static constexpr int TILE = 128 * D * 2;  // one operand tile
   static constexpr int NATOM = D / 64;      // 128-byte column slices
-  static constexpr int MISC = 1024;
-  static constexpr int SMEM = (2 + kTileStages) * TILE + MISC + 1024;
+  static constexpr int MISC = 512 + 2 * 2 * 128 * 4;  // barriers and records, row maxima
+  static constexpr int SMEM = (2 + kTileStages) * TILE + MISC;  // 231936 bytes at D = 128
   // one CTA per SM: it takes all 512 TMEM columns
   static constexpr int SMEM_LAUNCH = SMEM > 120 * 1024 ? SMEM : 120 * 1024;
 };
@@ -579,11 +582,12 @@ enum {
   TB_KV_EMPTY = TB_KV_FULL + kTileStages,
   TB_INFO = TB_KV_EMPTY + kTileStages,
   TB_Q = TB_INFO + kTileInfo,
-  TB_S,            // two: logits of a tile ready
-  TB_P = TB_S + 2,  // four: weights of a tile's keys 0..63 and 64..127 written
-  TB_O = TB_P + 4,  // two: output of a tile final
-  TB_DRAIN = TB_O + 2,
-  TB_COUNT
+  TB_S,             // four: logits of the keys 0..63 and 64..127 of a chunk ready, by tile
+  TB_P = TB_S + 4,  // four: their weights written
+  TB_X = TB_P + 4,  // eight: first maxima exchanged between a tile's halves, by 32 rows
+  TB_TAIL = TB_X + 8,      // value rows without a key in the last chunk are zeros
+  TB_DRAIN = TB_TAIL + 1,  // two
+  TB_COUNT = TB_DRAIN + 2
 };
 
 // How the tile kernel's work is cut. A request's rows make tile pairs of 256 rows, and a pair's
@@ -697,9 +701,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                       const PagedArgs a) {
   using Cfg = TileCfg<D>;
   constexpr bool kF16 = std::is_same<T, __half>::value;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t tile_smem[];  // swizzled tiles start on 1 KB
+  uint8_t* smem = tile_smem;
   const uint32_t sQ = smem_u32(smem), sKV = sQ + 2 * Cfg::TILE;
   uint8_t* misc = smem + (2 + kTileStages) * Cfg::TILE;
   uint64_t* bars = reinterpret_cast<uint64_t*>(misc);
@@ -708,12 +711,26 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ids + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* never = reinterpret_cast<int*>(tmem_slot + 2);
-  TileJob* where = reinterpret_cast<TileJob*>(tmem_slot + 3);  // r < 0: none
+  volatile int* redo = reinterpret_cast<volatile int*>(tmem_slot + 3);
+  TileJob* where = reinterpret_cast<TileJob*>(tmem_slot + 4);  // r < 0: none
+  static_assert(8 * TB_COUNT + kTileInfo * sizeof(TileInfo) + 8 * 4 + 4 * 4 + sizeof(TileJob) <= 512, "MISC");
+  volatile float* s_max = reinterpret_cast<volatile float*>(misc + 512);  // (tile, half, row)
   const uint32_t bar0 = smem_u32(bars);
 #define TBAR(i) (bar0 + 8u * static_cast<uint32_t>(i))
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.y;
+  auto init_barriers = [&](bool both) {
+    for (int i = 0; i < TB_COUNT; ++i) {
+      uint32_t n = 1;
+      if (i == TB_Q) n = 16;                       // softmax warps
+      if (i >= TB_KV_EMPTY && i < TB_KV_EMPTY + kTileStages) n = both ? 2 : 1;  // MMA warps
+      if (i >= TB_P && i < TB_P + 4) n = (i - TB_P) & 1 ? 4u : 5u;  // warps of a half; low: the stage warp too
+      if (i >= TB_X && i < TB_X + 8) n = 2;        // warps of 32 rows
+      mbar_init(TBAR(i), n);
+    }
+    fence_mbarrier_init();
+  };
 
   if (warp == 0) {
     TileJob job{};
@@ -727,11 +744,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int i = lane; i < a.R; i += 32) check_request(a, i);
   } else if (warp == 1) {
     if (lane == 0) {
-      for (int i = 0; i < TB_COUNT; ++i)
-        mbar_init(TBAR(i), i == TB_Q ? 8u : (i >= TB_P && i < TB_P + 4 ? 4u : 1u));  // by warp
       *abort_flag = 0;
       *never = 0;
-      fence_mbarrier_init();
+      *redo = 0;
       prefetch_tmap(&tmK);
       prefetch_tmap(&tmV);
     }
@@ -755,6 +770,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int row0 = where->tile * kTileRows, split = where->split, splits = where->splits;
   const int rows = min(kTileRows, q.n * a.G - row0);  // > 0
   const bool two = rows > 128;
+  if (tid == 0) init_barriers(two);
+  __syncthreads();
   // keys that the CTA's last row sees, and this split's share of them in 128-key steps
   const int last_tok = (row0 + rows - 1) / a.G;
   const int key_end = a.causal ? min(q.len, q.ctx + last_tok + 1) : q.len;
@@ -765,7 +782,44 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   auto wait_all = [&](uint32_t bar, uint32_t parity, int site) -> bool {
     return __all_sync(0xffffffffu, mbar_wait_poll(bar, parity, abort_flag, site));
   };
-  if (warp == 9) {
+  // Softmax: two threads per row, one for each half of a chunk's 128 keys (two warpgroups per
+  // tile, four softmax warps on each scheduler, so that one's arithmetic runs under another's
+  // exponentials). A row's weights are relative to the largest logit of the first chunk, fixed
+  // for good: nothing of a chunk waits for its maximum, and the output is never rescaled. That
+  // is safe while no later logit is more than kExcess above it (base-2 units; the weights stay in
+  // the type's range, and sums and outputs far inside fp32's). Each thread keeps the largest
+  // logit that it saw; if some row went past the limit, the whole CTA does its work once
+  // more, relative to the rows' largest logits of all, which cannot fail.
+  constexpr float kExcess = kF16 ? 14.f : 60.f;
+  const int t = (warp >> 3) & 1, hb = (warp >> 2) & 1, rr = tid & 127;
+  const int row = row0 + 128 * t + rr;
+  const bool live = warp < 16 && 128 * t + rr < rows;
+  const int tok = row / a.G, hq = h * a.G + row % a.G;
+  const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  const uint32_t tO = tmem + 256 + 128 * t + (D / 2) * hb + lanes;  // this half's output columns
+  // Rows of a warp move whole, UN lanes of 16 bytes to a row: with a lane per row every access
+  // touched 32 lines, 4000 cycles of Q and 8000 of partial results for a CTA.
+  constexpr int UN = D / 8;
+  const int u = lane % UN;
+  auto other_row = [&](const void* p, int r) {
+    return reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(p), r));
+  };
+  float m_row = -INFINITY, l_run = 0.f;
+  int nch = 0;
+  bool ok_all = true;
+  // The end of a pass, for every thread of the CTA: true when it was the last one.
+  auto last_pass = [&](int pass) -> bool {
+    tc_fence_before();
+    named_bar_sync(1, kTileThreads);
+    tc_fence_after();
+    return pass == 1 || *redo == 0;
+  };
+  if (warp >= 16) {
+  // registers go from the last warpgroup to the softmax warpgroups
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+#pragma unroll 1
+  for (int pass = 0;; ++pass) {
+  if (warp == 17) {
     // ------------------------------------------------ TMA warp: gathers chunks page by page
     // A load takes lu = min(page, 128) rows; chunk = 128 / lu loads of kept pages, in order.
     const int lu_shift = min(a.page_shift, 7), lu = 1 << lu_shift, per_chunk = 128 >> lu_shift;
@@ -789,7 +843,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     int base = key_lo >> lu_shift;
     int id = look(base), id_next = look(base + 32);
     unsigned left = __ballot_sync(0xffffffffu, id >= 0);
-    uint32_t loads = 0;  // stages filled so far
+    uint32_t loads = 0;   // stages filled so far
+    int tail_rows = 128;  // rows that hold keys in the last chunk (all in those before it)
     bool ok = true;
     for (int j = 0; ok; ++j) {
       // (the record is free: the stage of the last chunk's keys was last used by the values of
@@ -827,6 +882,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(TBAR(TB_INFO + j % kTileInfo));
       if (filled == 0) break;
+      tail_rows = valid;
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
         const uint32_t stage = loads % kTileStages;
@@ -848,128 +904,168 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ++loads;
       }
     }
+    // value rows without a key in the last chunk: zeros (what lies there may be anything, and
+    // 0 * NaN is NaN)
+    if (ok && tail_rows < 128) {
+      const uint32_t stage = (loads - 1) % kTileStages;
+      ok = wait_all(TBAR(TB_KV_FULL + stage), ((loads - 1) / kTileStages) & 1, kPagedSite + 13);
+      if (ok) {
+        for (int i = tail_rows * 8 + lane; i < 128 * 8; i += 32)
+#pragma unroll
+          for (int cc = 0; cc < Cfg::NATOM; ++cc)
+            *reinterpret_cast<uint4*>(smem + (2 + stage) * Cfg::TILE + cc * 16384 + i * 16) =
+                make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(TBAR(TB_TAIL));
+      }
+    }
     // every copy has landed before the CTA may end
     for (uint32_t i = loads > kTileStages ? loads - kTileStages : 0; i < loads; ++i)
       mbar_wait_poll(TBAR(TB_KV_FULL + i % kTileStages), (i / kTileStages) & 1, never, kPagedSite + 12);
-  } else if (warp == 8) {
-    // ------------------------------------------------ MMA warp
-    // Tile t's logits and, over them, its weights live in TMEM columns 128 t .., its output in
-    // 256 + 128 t ... While the softmax warps of one tile are at work, the other tile's
-    // products run: PV(t, j) then QK(t, j + 1), for t = 0 and 1 in turn.
+  } else if (warp == 16 || (warp == 18 && two)) {
+    // ------------------------------------------------ MMA warps, one per tile
+    // The two halves of a chunk's keys are pipelines of their own: logits (and over them, their
+    // weights) in TMEM columns 128 t + 64 half, the output of both in columns 256 + 128 t. A
+    // half's next logits go where its weights were, QK(j + 1, half) right behind PV(j, half).
+    // So four pipelines (two tiles, two halves) keep the tensor core and the exponentials busy
+    // between them. A warp per tile, because a warp that has committed stands still until its
+    // products are done; the whole warp runs on uniform values, so that descriptors live in
+    // uniform registers (a lone thread took 75 cycles to issue a product that takes 64).
+    const int t = warp == 18 ? 1 : 0;
     auto commit = [&](uint32_t bar) {
       if (elect_one()) tc_commit(bar);
       __syncwarp();
     };
-    constexpr uint32_t kIdQK = make_idesc16(kF16, 128, 128, false, false);
+    constexpr uint32_t kIdQK = make_idesc16(kF16, 128, 64, false, false);
     constexpr uint32_t kIdPV = make_idesc16(kF16, 128, D, false, true);
-    const uint64_t dQ = smem_desc(sQ, 16, 1024);
+    const uint64_t dQ = smem_desc(sQ + t * Cfg::TILE, 16, 1024);
     const uint64_t dKV = smem_desc(sKV, 16, 1024);
     const uint64_t dV = smem_desc(sKV, 16384, 1024);
-    auto issue_qk = [&](int t, uint32_t stage) {
+    const uint32_t tS = tmem + 128 * t, tO = tmem + 256 + 128 * t;
+    auto issue_qk = [&](int half, uint32_t stage) {
+      const uint64_t kd = dKV + static_cast<uint64_t>((stage * Cfg::TILE + half * 64 * 128) >> 4);
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t off = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-          mma_ss<false>(tmem + 128 * t, dQ + static_cast<uint64_t>((t * Cfg::TILE) >> 4) + off,
-                        dKV + static_cast<uint64_t>((stage * Cfg::TILE) >> 4) + off, kIdQK, kk > 0 ? 1u : 0u);
+          mma_ss<false>(tS + 64 * half, dQ + off, kd + off, kIdQK, kk > 0 ? 1u : 0u);
         }
       }
       __syncwarp();
     };
-    auto issue_pv = [&](int t, int half, uint32_t stage, bool first) {
+    auto issue_pv = [&](int half, uint32_t stage, bool first) {
+      const uint64_t vd = dV + static_cast<uint64_t>((stage * Cfg::TILE + half * 4 * 2048) >> 4);
       if (elect_one()) {
 #pragma unroll
-        for (int k4 = 0; k4 < 4; ++k4) {
-          const int kk = 4 * half + k4;
-          mma_ts<false>(tmem + 256 + 128 * t, tmem + 128 * t + kk * 8,
-                        dV + static_cast<uint64_t>((stage * Cfg::TILE + kk * 2048) >> 4), kIdPV,
-                        (!first || kk > 0) ? 1u : 0u);
-        }
+        for (int k4 = 0; k4 < 4; ++k4)
+          mma_ts<false>(tO, tS + 64 * half + k4 * 8, vd + static_cast<uint64_t>((k4 * 2048) >> 4), kIdPV,
+                        (!first || k4 > 0) ? 1u : 0u);
       }
       __syncwarp();
     };
-    bool ok = wait_all(TBAR(TB_Q), 0, kPagedSite + 20);
+    uint32_t vst = 1, kst = 2;  // stages of V(j) and K(j + 1)
+    bool ok = pass > 0 || wait_all(TBAR(TB_Q), 0, kPagedSite + 20);
     ok = ok && wait_all(TBAR(TB_INFO), 0, kPagedSite + 21);
-    int chunk_rows = ok ? info[0].rows : 0;
-    if (ok && chunk_rows > 0) {
-      ok = wait_all(TBAR(TB_KV_FULL), 0, kPagedSite + 22);
-      if (ok) {
-        tc_fence_after();
-        for (int t = 0; t < (two ? 2 : 1); ++t) {
-          issue_qk(t, 0);
-          commit(TBAR(TB_S + t));
-        }
-        commit(TBAR(TB_KV_EMPTY));
+    int rows_j = ok ? info[0].rows : 0;
+    if (ok && rows_j > 0 && (ok = wait_all(TBAR(TB_KV_FULL), 0, kPagedSite + 22))) {
+      tc_fence_after();
+      issue_qk(0, 0);
+      commit(TBAR(TB_S + 2 * t));
+      if (rows_j > 64) {
+        issue_qk(1, 0);
+        commit(TBAR(TB_S + 2 * t + 1));
       }
+      commit(TBAR(TB_KV_EMPTY));
     }
-    uint32_t load = 1;  // next stage to use: the values of chunk 0
-    for (int j = 0; ok && chunk_rows > 0; ++j) {
-      const uint32_t vst = load % kTileStages, vph = (load / kTileStages) & 1;
-      const uint32_t kst = (load + 1) % kTileStages, kph = ((load + 1) / kTileStages) & 1;
-      load += 2;
-      if (!(ok = wait_all(TBAR(TB_KV_FULL + vst), vph, kPagedSite + 23))) break;
-      if (chunk_rows < 128) {
-        // value rows without a key: zeros (what lies there may be anything, and 0 * NaN is NaN)
-        for (int i = chunk_rows * 8 + lane; i < 128 * 8; i += 32)
-#pragma unroll
-          for (int cc = 0; cc < Cfg::NATOM; ++cc)
-            *reinterpret_cast<uint4*>(smem + (2 + vst) * Cfg::TILE + cc * 16384 + i * 16) =
-                make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      if (!(ok = wait_all(TBAR(TB_INFO + (j + 1) % kTileInfo), ((j + 1) / kTileInfo) & 1, kPagedSite + 24))) break;
+    for (int j = 0; ok && rows_j > 0; ++j) {
+      // low half: its weights, V(j) and K(j + 1) are there
+      if (!(ok = wait_all(TBAR(TB_P + 2 * t), j & 1, kPagedSite + 25))) break;
+      tc_fence_after();
+      issue_pv(0, vst, j == 0);
       const int next_rows = info[(j + 1) % kTileInfo].rows;
-      for (int t = 0; ok && t < (two ? 2 : 1); ++t) {
-        if (!(ok = wait_all(TBAR(TB_P + 2 * t), j & 1, kPagedSite + 25))) break;
-        tc_fence_after();
-        issue_pv(t, 0, vst, j == 0);
-        if (!(ok = wait_all(TBAR(TB_P + 2 * t + 1), j & 1, kPagedSite + 28))) break;
-        tc_fence_after();
-        issue_pv(t, 1, vst, j == 0);
-        if (t == (two ? 1 : 0)) commit(TBAR(TB_KV_EMPTY + vst));
-        if (next_rows > 0) {
-          if (t == 0 && !(ok = wait_all(TBAR(TB_KV_FULL + kst), kph, kPagedSite + 26))) break;
-          tc_fence_after();
-          issue_qk(t, kst);
-          commit(TBAR(TB_S + t));
-        } else {
-          commit(TBAR(TB_O + t));
-        }
+      if (next_rows > 0) {
+        issue_qk(0, kst);
+        commit(TBAR(TB_S + 2 * t));
       }
+      if (rows_j <= 64) break;     // (the last chunk)
+      // high half
+      if (!(ok = wait_all(TBAR(TB_P + 2 * t + 1), j & 1, kPagedSite + 28))) break;
+      tc_fence_after();
+      issue_pv(1, vst, false);
+      if (next_rows > 64) {
+        issue_qk(1, kst);
+        commit(TBAR(TB_S + 2 * t + 1));
+      }
+      commit(TBAR(TB_KV_EMPTY + vst));
       if (next_rows > 0) commit(TBAR(TB_KV_EMPTY + kst));
-      chunk_rows = next_rows;
+      rows_j = next_rows;
+      vst = vst + 2 >= kTileStages ? vst + 2 - kTileStages : vst + 2;
+      kst = kst + 2 >= kTileStages ? kst + 2 - kTileStages : kst + 2;
     }
     // every product has completed before the CTA may end
-    commit(TBAR(TB_DRAIN));
-    mbar_wait_poll(TBAR(TB_DRAIN), 0, never, kPagedSite + 27);
+    commit(TBAR(TB_DRAIN + t));
+    mbar_wait_poll(TBAR(TB_DRAIN + t), 0, never, kPagedSite + 27);
+  } else if (warp == 19) {
+    // ------------------------------------------------ stage warp
+    // A wait costs a warp 250 to 350 cycles here even when there is nothing to wait for, and the
+    // MMA warps' instructions are what a chunk's time consists of; so this warp waits for
+    // V(j), the next record and K(j + 1) in their place, and its arrival is one of those that
+    // complete the low half's weights.
+    uint32_t vst = 1, vph = 0, kst = 2, kph = 0;
+    bool ok = wait_all(TBAR(TB_INFO), 0, kPagedSite + 36);
+    int rows_j = ok ? info[0].rows : 0;
+    for (int j = 0; ok && rows_j > 0; ++j) {
+      if (!(ok = wait_all(TBAR(TB_KV_FULL + vst), vph, kPagedSite + 23))) break;
+      if (rows_j < 128 && !(ok = wait_all(TBAR(TB_TAIL), 0, kPagedSite + 35))) break;
+      if (!(ok = wait_all(TBAR(TB_INFO + (j + 1) % kTileInfo), ((j + 1) / kTileInfo) & 1, kPagedSite + 24))) break;
+      rows_j = info[(j + 1) % kTileInfo].rows;
+      if (rows_j > 0 && !(ok = wait_all(TBAR(TB_KV_FULL + kst), kph, kPagedSite + 26))) break;
+      if (j > 0) {  // one arrival in each phase
+        ok = wait_all(TBAR(TB_P), (j - 1) & 1, kPagedSite + 37);
+        if (ok && two) ok = wait_all(TBAR(TB_P + 2), (j - 1) & 1, kPagedSite + 37);
+        if (!ok) break;
+      }
+      if (lane == 0) {
+        mbar_arrive(TBAR(TB_P));
+        if (two) mbar_arrive(TBAR(TB_P + 2));
+      }
+      __syncwarp();
+      vst += 2;
+      if (vst >= kTileStages) { vst -= kTileStages; vph ^= 1u; }
+      kst += 2;
+      if (kst >= kTileStages) { kst -= kTileStages; kph ^= 1u; }
+    }
+  }
+  if (last_pass(pass)) break;
+  if (tid == 512) {
+    for (int i = 0; i < TB_COUNT; ++i) mbar_inval(TBAR(i));
+    init_barriers(two);
+  }
+  named_bar_sync(1, kTileThreads);
+  }
   } else {
-    // ------------------------------------------------ softmax: one thread per row
-    const int t = warp >> 2, rr = tid & 127;
-    const int row = row0 + 128 * t + rr;
-    const bool live = 128 * t + rr < rows;
-    const int tok = row / a.G, hq = h * a.G + row % a.G;
-    // Rows of a warp move whole, UN lanes of 16 bytes to a row: with a lane per row every access
-    // touched 32 lines, 4000 cycles of Q and 8000 of partial results for a CTA.
-    constexpr int UN = D / 8;
-    const int u = lane % UN;
-    auto row_of = [&](int i) { return i * (32 / UN) + lane / UN; };  // of the warp's 32
-    auto other_row = [&](const void* p, int r) {
-      return reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(p), r));
-    };
-    // this warp's rows of Q into the swizzled tile (16-byte piece u of row r at u ^ (r & 7))
-    {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+#pragma unroll 1
+  for (int pass = 0;; ++pass) {
+    // ------------------------------------------------ softmax
+    const uint32_t tS = tmem + 128 * t + 64 * hb + lanes;  // this half's logits and weights
+    const uint32_t xbar = TBAR(TB_X + 4 * t + (warp & 3));
+    volatile float* xmine = s_max + (t * 2 + hb) * 128 + rr;
+    const volatile float* xother = s_max + (t * 2 + (hb ^ 1)) * 128 + rr;
+    if (pass == 0) {
+      // half of this warp's rows of Q into the swizzled tile (16-byte piece u of row r at u ^ (r & 7))
       const T* src = static_cast<const T*>(a.q) + hq * a.qh + static_cast<int64_t>(q.t0 + tok) * a.qt;
-      uint4 v[UN];
+      uint4 v[UN / 2];
 #pragma unroll
-      for (int i = 0; i < UN; ++i) {
-        const int r = row_of(i);
+      for (int i = 0; i < UN / 2; ++i) {
+        const int r = hb * 16 + i * (32 / UN) + lane / UN;
         const uint8_t* p = other_row(src, r) + 16 * u;
         v[i] = 128 * t + (warp & 3) * 32 + r < rows ? ldg_stream(p) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int i = 0; i < UN; ++i) {
-        const int r = (warp & 3) * 32 + row_of(i);
+      for (int i = 0; i < UN / 2; ++i) {
+        const int r = (warp & 3) * 32 + hb * 16 + i * (32 / UN) + lane / UN;
         *reinterpret_cast<uint4*>(smem + t * Cfg::TILE + (u >> 3) * 16384 + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = v[i];
       }
       fence_proxy_async_smem();
@@ -979,143 +1075,140 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int lim = live ? (a.causal ? min(q.len - 1, q.ctx + tok) : q.len - 1) : -1;
     // the smallest reach of the tile's rows (its first row's): chunks up to it need no mask
     const int lim_tile = a.causal ? min(q.len - 1, q.ctx + (row0 + 128 * t) / a.G) : q.len - 1;
-    const uint32_t tS = tmem + 128 * t + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t tO = tS - 128 * t + 256 + 128 * t;
-    float m_run = -INFINITY, l_run = 0.f;
+    float seen = -INFINITY;  // largest logit (times the scale, base 2)
     bool ok = t == 0 || two;
-    int nch = 0;
+    l_run = 0.f;
+    nch = 0;
 #pragma unroll 1
     for (int j = 0; ok; ++j) {
       if (!(ok = wait_all(TBAR(TB_INFO + j % kTileInfo), (j / kTileInfo) & 1, kPagedSite + 30))) break;
       const TileInfo* ti = info + j % kTileInfo;
       if (ti->rows == 0) break;
-      const bool edge = ti->last > lim_tile;
-      if (!(ok = wait_all(TBAR(TB_S + t), j & 1, kPagedSite + 31))) break;
-      tc_fence_after();
+      const bool edge = ti->last > lim_tile, has = ti->rows > 64 * hb;
       ++nch;
-      float v[4][32];
+      float v[2][32];
+      if (has) {
+        if (!(ok = wait_all(TBAR(TB_S + 2 * t + hb), j & 1, kPagedSite + 31))) break;
+        tc_fence_after();
+        tmem_ld32(tS, v[0]);
+        tmem_ld32(tS + 32, v[1]);
+        tmem_wait_ld();
+        if (edge) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, v[i]);
-      tmem_wait_ld();
-      if (edge) {
+          for (int i = 0; i < 4; ++i) {
+            const int vis = lim - ti->pos[4 * hb + i];  // last visible column of the granule
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int seen = lim - ti->pos[i];  // last visible column of the granule
-#pragma unroll
-          for (int c = 0; c < 16; ++c)
-            if (c > seen) v[i >> 1][(i & 1) * 16 + c] = -INFINITY;
-        }
-      }
-      float mx = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mx = max3(mx, max16(v[i]), max16(v[i] + 16));
-      mx *= a.scale_log2;
-      // Lazy rescaling: the running maximum moves when it is passed by more than 8 (base-2
-      // units), so the weights stay below 2^8 and the output is rarely touched. The logits'
-      // commit came after the previous product of this tile, so the output is at rest.
-      const bool need = mx > m_run + 8.f;
-      if (__any_sync(0xffffffffu, need)) {
-        float alpha = 1.f;
-        if (need) {
-          alpha = ex2(m_run - mx);
-          l_run *= alpha;
-          m_run = mx;
-        }
-        if (j > 0) {
-#pragma unroll 1
-          for (int p = 0; p < D / 32; ++p) {
-            float o[32];
-            tmem_ld32(tO + p * 32, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] *= alpha;
-            tmem_st32(tO + p * 32, *reinterpret_cast<uint32_t(*)[32]>(o));
+            for (int c = 0; c < 16; ++c)
+              if (c > vis) v[i >> 1][(i & 1) * 16 + c] = -INFINITY;
           }
         }
       }
-      const float neg = m_run == -INFINITY ? 0.f : -m_run;
-      float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
+      if (j == 0 && pass == 0) {  // the reference, of both halves
+        *xmine = has ? max64(v[0], v[1]) * a.scale_log2 : -INFINITY;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(xbar);
+        if (!(ok = wait_all(xbar, 0, kPagedSite + 33))) break;
+        m_row = fmaxf(*xmine, *xother);
+      }
+      if (!has) break;  // (the last chunk)
+      const float neg = m_row == -INFINITY ? 0.f : -m_row;
+      float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f, q0 = -INFINITY, q1 = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         uint32_t w[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
           float x0, x1;
           fma2(x0, x1, v[i][2 * c], v[i][2 * c + 1], a.scale_log2, a.scale_log2, neg, neg);
+          if (c & 1) q1 = max3(q1, x0, x1);
+          else q0 = max3(q0, x0, x1);
           x0 = ex2(x0);
           x1 = ex2(x1);
-          if (c & 1) add2(sb0, sb1, sb0, sb1, x0, x1);
-          else add2(sa0, sa1, sa0, sa1, x0, x1);
+          if (c & 1) add2(s2, s3, s2, s3, x0, x1);
+          else add2(s0, s1, s0, s1, x0, x1);
           w[c] = pack_pair<T>(x0, x1);
         }
         tmem_st16(tS + 16 * i, w);
-        if (i & 1) {  // half of the keys: their product may start
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(TBAR(TB_P + 2 * t + (i >> 1)));
-        }
       }
-      l_run += (sa0 + sa1) + (sb0 + sb1);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(TBAR(TB_P + 2 * t + hb));
+      l_run += (s0 + s1) + (s2 + s3);
+      seen = max3(seen, q0, q1);  // relative to the row's reference
     }
-    if (ok && nch > 0) ok = wait_all(TBAR(TB_O + t), 0, kPagedSite + 32);
-    if (ok && (t == 0 || two)) {
-      tc_fence_after();
-      // out through the tile's Q, which no product reads any more: each lane's row (in 16-byte
-      // pieces, piece u of row r at u ^ r), then row by row
-      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-      uint8_t* stage = smem + t * Cfg::TILE + (warp & 3) * (Cfg::TILE / 4);
-      const size_t prow = splits > 1 ? tile_part_row(a, where->slot + split, h, 128 * t + rr) : 0;
-      auto put = [&](int piece, const uint4& x) {
-        *reinterpret_cast<uint4*>(stage + lane * (2 * D) + ((piece ^ (lane & (UN - 1))) << 4)) = x;
-      };
-      auto drain = [&](void* row_ptr) {
-        __syncwarp();
+    ok_all = ok || !(t == 0 || two);
+    // A row that the reference is too low for: its largest logit of all goes to both halves.
+    if (__any_sync(0xffffffffu, seen > kExcess) && lane == 0) *redo = 1;
+    *xmine = seen;
+    if (last_pass(pass)) break;
+    const float most = fmaxf(seen, *xother);
+    if (m_row > -INFINITY) m_row += fmaxf(most, 0.f);
+    named_bar_sync(1, kTileThreads);
+  }
+  // (every product and copy has ended) the sums of a row's halves, through the first stage
+  volatile float* sums = reinterpret_cast<volatile float*>(smem + 2 * Cfg::TILE);
+  sums[(t * 2 + hb) * 128 + rr] = l_run;
+  named_bar_sync(2, 512);
+  if (ok_all && (t == 0 || two)) {
+    l_run = sums[t * 256 + rr] + sums[t * 256 + 128 + rr];
+    // Out through the tile's Q, which no product reads any more: each lane's half row in pieces of
+    // 16 bytes (piece x of row r at x ^ r), then row by row. A warp has 32 rows of D bytes.
+    constexpr int UH = D / 16;  // pieces of a row
+    const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+    uint8_t* stage = smem + t * Cfg::TILE + (warp & 7) * (Cfg::TILE / 8);
+    const int uh = lane % UH;
+    auto put = [&](int piece, const uint4& x) {
+      *reinterpret_cast<uint4*>(stage + lane * D + ((piece ^ (lane & (UH - 1))) << 4)) = x;
+    };
+    auto drain = [&](void* row_ptr) {
+      __syncwarp();
 #pragma unroll 4
-        for (int i = 0; i < UN; ++i) {
-          const int r = row_of(i);
-          uint8_t* p = other_row(row_ptr, r);
-          const uint4 x = *reinterpret_cast<const uint4*>(stage + r * (2 * D) + ((u ^ (r & (UN - 1))) << 4));
-          if (128 * t + (warp & 3) * 32 + r < rows) *reinterpret_cast<uint4*>(p + 16 * u) = x;
-        }
-        __syncwarp();
-      };
-      auto take = [&](int col, float(&o)[32]) {
-        if (nch > 0) {
-          tmem_ld32(tO + col, o);
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = 0.f;
-        }
-      };
-      if (splits > 1) {  // unnormalised fp32, half of the columns at a time
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-#pragma unroll
-          for (int p = 0; p < D / 64; ++p) {
-            float o[32];
-            take(half * (D / 2) + p * 32, o);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) put(8 * p + c, *reinterpret_cast<uint4*>(o + 4 * c));
-          }
-          drain(a.part + prow * D + half * (D / 2));
-        }
+      for (int i = 0; i < UH; ++i) {
+        const int r = i * (32 / UH) + lane / UH;
+        uint8_t* p = other_row(row_ptr, r);
+        const uint4 x = *reinterpret_cast<const uint4*>(stage + r * D + ((uh ^ (r & (UH - 1))) << 4));
+        if (128 * t + (warp & 3) * 32 + r < rows) *reinterpret_cast<uint4*>(p + 16 * uh) = x;
+      }
+      __syncwarp();
+    };
+    auto take = [&](int col, float(&o)[16]) {
+      if (nch > 0) {
+        tmem_ld16(tO + col, o);
+        tmem_wait_ld();
       } else {
 #pragma unroll
-        for (int p = 0; p < D / 32; ++p) {
-          float o[32];
-          take(p * 32, o);
-          uint32_t w[16];
-#pragma unroll
-          for (int c = 0; c < 16; ++c) w[c] = l_run > 0.f ? pack_pair<T>(o[2 * c] * inv, o[2 * c + 1] * inv) : 0u;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) put(4 * p + c, make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]));
-        }
-        drain(static_cast<T*>(a.out) + hq * a.oh + static_cast<int64_t>(q.t0 + tok) * a.ot);
+        for (int c = 0; c < 16; ++c) o[c] = 0.f;
       }
-      if (live && splits > 1) *reinterpret_cast<float2*>(tile_part_ml(a, D) + prow * 2) = make_float2(m_run, l_run);
+    };
+    if (splits > 1) {  // unnormalised fp32, D bytes of a row at a time
+      const size_t prow = tile_part_row(a, where->slot + split, h, 128 * t + rr);
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int p = 0; p < D / 64; ++p) {
+          float o[16];
+          take(half * (D / 4) + p * 16, o);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) put(4 * p + c, *reinterpret_cast<uint4*>(o + 4 * c));
+        }
+        drain(a.part + prow * D + hb * (D / 2) + half * (D / 4));
+      }
+      if (live && hb == 0) *reinterpret_cast<float2*>(tile_part_ml(a, D) + prow * 2) = make_float2(m_row, l_run);
+    } else {
+#pragma unroll
+      for (int p = 0; p < D / 32; ++p) {
+        float o[16];
+        take(p * 16, o);
+        uint32_t w[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) w[c] = l_run > 0.f ? pack_pair<T>(o[2 * c] * inv, o[2 * c + 1] * inv) : 0u;
+        put(2 * p, make_uint4(w[0], w[1], w[2], w[3]));
+        put(2 * p + 1, make_uint4(w[4], w[5], w[6], w[7]));
+      }
+      drain(static_cast<T*>(a.out) + hq * a.oh + static_cast<int64_t>(q.t0 + tok) * a.ot + hb * (D / 2));
     }
+  }
   }
 #undef TBAR
   tc_fence_before();
@@ -1200,7 +1293,7 @@ struct PagedPlan {
   bool token, tile;  // which kernels run
   int min_rows;      // rows up to which a request is the token kernel's
   int workers, one_each;
-  int tile_ctas, can_split;
+  int tile_ctas, can_split, join_pairs;
   size_t bytes;
   size_t tile_off;
 };
@@ -1227,6 +1320,7 @@ PagedPlan paged_plan(int R, int T, int Hq, int Hkv, int D, int max_new, int widt
     const int64_t pairs = static_cast<int64_t>(T) * G / kTileRows + std::min(R, T);
     p.can_split = keys > kTileMinChunks * 128;
     p.tile_ctas = static_cast<int>(pairs + (p.can_split ? ceil_div(kTileJobs, Hkv) : 0));
+    p.join_pairs = static_cast<int>(std::min<int64_t>(pairs, ceil_div(kTileJobs, Hkv)));
     if (p.can_split) b += align_up(static_cast<size_t>(kTileSlots) * kTileRows * (D + 2) * sizeof(float), 256);
   }
   p.bytes = std::max<size_t>(b, 256);
@@ -1312,7 +1406,7 @@ int launch_paged(PagedArgs a, const PagedPlan& p, const bsa_paged_cache& c, char
     count_launch();
     if (p.can_split) {
       e = check_cuda(launch_dependent(tile_combine_kernel<T, D>,
-                                      dim3(ceil_div(kTileJobs, a.Hkv) * a.Hkv, kTileRows / tile_join_rows<D>()),
+                                      dim3(p.join_pairs * a.Hkv, kTileRows / tile_join_rows<D>()),
                                       dim3(kJoinThreads), 0, st, t), "tile_combine_kernel");
       if (e != BSA_OK) return e;
       count_launch();

@@ -270,6 +270,23 @@ def test_chunks(dt, D, causal, Hq, Hkv, page, ctx, new):
     _run(ctx, new, Hq, Hkv, D, page, dt, causal)
 
 
+@pytest.mark.parametrize("dt,D", [("bf16", 128), ("bf16", 64), ("f16", 128), ("f16", 64)])
+@pytest.mark.parametrize("ctx,new,causal", [([300], [40], True), ([0], [300], True), ([2300], [20], False)])
+def test_chunks_whose_logits_rise(dt, D, ctx, new, causal):
+    """Later keys whose logits are far above the first ones' (a hundred and more base-2 units in
+    some rows, a little in others), rows that see only the first ones beside them."""
+    bsa = _bsa()
+    q, kc, vc, table, cu, _ = _attention_case(40, ctx, new, 2, 1, D, 64, TYPES[dt], None, 1.0, False, True)
+    order = table[0]
+    for j in range(3, len(order)):
+        kc[order[j]] *= 1.0 + 2.0 * (j % 4)
+    q[:, ::5] *= 4.0
+    out = torch.full_like(q, 7.0)
+    bsa.paged_chunk_attention(q, kc, vc, _i32(table), _i32(cu), _i32(ctx), causal=causal, max_new=max(new), out=out)
+    assert bsa.device_status() == (0, 0) and (out[:, cu[-1]:] == 7.0).all()
+    _check(out, q, kc, vc, table, cu, ctx, causal, None)
+
+
 def test_chunks_split_keys():
     _run([2500], [20], 2, 1, 128, 64, "bf16", True, seed=5, gain=3.0)
     _run([4200], [9], 2, 1, 64, 16, "f16", False, seed=6)
