@@ -46,7 +46,7 @@ def _native_command(out):
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             *[x for i in inc for x in ("-isystem", i)], NATIVE_SRC, "-o", out,
             "-L", HERE, "-l:libbsa.so", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(t, "lib"),
-            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+            "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
 
 
 def _compile(cmd, out, verbose):

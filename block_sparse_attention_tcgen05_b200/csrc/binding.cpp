@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -230,10 +231,17 @@ Norm expect_norm(const at::Tensor& q, const at::Tensor& k, const at::Tensor& qw,
 template <class T>
 T* ptr(const at::Tensor* t) { return t ? static_cast<T*>(t->data_ptr()) : nullptr; }
 
+// Uninitialised tensors straight from the CUDA allocator (the dispatcher costs as much again).
+at::Tensor empty(at::IntArrayRef size, at::ScalarType dt, c10::Device dev) {
+  return at::Tensor(at::detail::empty_cuda(size, dt, dev, std::nullopt));
+}
+at::Tensor empty_strided(at::IntArrayRef size, at::IntArrayRef stride, at::ScalarType dt, c10::Device dev) {
+  return at::Tensor(at::detail::empty_strided_cuda(size, stride, dt, dev));
+}
+
 at::Tensor workspace_or_new(const at::Tensor* ws, size_t need, c10::Device dev) {
   if (ws && static_cast<size_t>(ws->numel()) >= need) return *ws;
-  return at::empty({static_cast<int64_t>(std::max<size_t>(need, 256))},
-                   at::TensorOptions().dtype(at::kByte).device(dev));
+  return empty({static_cast<int64_t>(std::max<size_t>(need, 256))}, at::kByte, dev);
 }
 
 void expect_workspace(const at::Tensor* ws) {
@@ -278,8 +286,8 @@ PyObject* norm(PyObject* const* a) {
   }
   const bsa_heads hq = heads(q, "q"), hk = heads(k, "k");
   const c10::Device dev = same_device({&q, &k, &qw, &kw, &cos, &sin, pos, qo, ko});
-  const at::Tensor q_out = qo ? *qo : at::empty(q.sizes(), q.options());
-  const at::Tensor k_out = ko ? *ko : at::empty(k.sizes(), k.options());
+  const at::Tensor q_out = qo ? *qo : empty(q.sizes(), q.scalar_type(), dev);
+  const at::Tensor k_out = ko ? *ko : empty(k.sizes(), k.scalar_type(), dev);
   const bsa_heads oq = heads(q_out, "q_out", true), ok = heads(k_out, "k_out", true);
   const float eps = number(a[7]);
   const int inter = truth(a[8]);
@@ -292,11 +300,10 @@ PyObject* norm(PyObject* const* a) {
 
 // An empty tensor of t's shape, token-major in memory where t is, else contiguous.
 at::Tensor like_layout(const at::Tensor& t) {
-  const int64_t B = t.size(0), H = t.size(1), S = t.size(2), D = t.size(3);
-  (void)B;
+  const int64_t H = t.size(1), S = t.size(2), D = t.size(3);
   if (H > 1 && S > 1 && t.stride(1) < t.stride(2))
-    return at::empty_strided(t.sizes(), {H * S * D, D, H * D, 1}, t.options());
-  return at::empty(t.sizes(), t.options());
+    return empty_strided(t.sizes(), {H * S * D, D, H * D, 1}, t.scalar_type(), t.device());
+  return empty(t.sizes(), t.scalar_type(), t.device());
 }
 
 PyObject* norm_back(PyObject* const* a) {
@@ -314,8 +321,7 @@ PyObject* norm_back(PyObject* const* a) {
   const c10::Device dev = same_device({&dqo, &dko, &q, &k, &qw, &kw, &cos, &sin, pos, ws});
   const at::Tensor work = workspace_or_new(ws, bsa_qk_norm_rotation_workspace_bytes(n.shape), dev);
   const at::Tensor dq = like_layout(q), dk = like_layout(k);
-  const auto f32 = q.options().dtype(at::kFloat);
-  const at::Tensor dqw = at::empty({q.size(3)}, f32), dkw = at::empty({q.size(3)}, f32);
+  const at::Tensor dqw = empty({q.size(3)}, at::kFloat, dev), dkw = empty({q.size(3)}, at::kFloat, dev);
   const bsa_heads oq = heads(dq, "dq", true), ok = heads(dk, "dk", true);
   const float eps = number(a[9]);
   const int inter = truth(a[10]);
@@ -353,9 +359,8 @@ PyObject* tables(PyObject* const* a) {
   const int T = integer32(a[4], "n_tokens"), page = integer32(a[5], "page_size"), n_pages = integer32(a[6], "n_pages");
   if (T < 0) bad("n_tokens < 0");
   const c10::Device dev = same_device({&ctx, &nl, &bt, &fp});
-  const auto opt = ctx.options();
-  const at::Tensor slots = at::empty({T}, opt), positions = at::empty({T}, opt), cu = at::empty({R + 1}, opt),
-                   taken = at::empty({1}, opt);
+  const at::Tensor slots = empty({T}, at::kInt, dev), positions = empty({T}, at::kInt, dev),
+                   cu = empty({R + 1}, at::kInt, dev), taken = empty({1}, at::kInt, dev);
   launch("bsa_paged_block_tables", dev, [&](void* st) {
     return bsa_paged_block_tables(ptr<int32_t>(&ctx), ptr<int32_t>(&nl), as_int(R, "context_lens"), ptr<int32_t>(&bt),
                                   as_int(bt.size(1), "block_table"), stride, ptr<int32_t>(&fp),
@@ -431,7 +436,7 @@ PyObject* append(PyObject* const* a) {
   }
   const bsa_heads hq = heads(q, "q"), hk = heads(k, "k"), hv = heads(v, "v");
   const c10::Device dev = same_device({&q, &k, &v, &qw, &kw, &cos, &sin, &pos, &slots, &kc, &vc, qo});
-  const at::Tensor q_out = qo ? *qo : at::empty(q.sizes(), q.options());
+  const at::Tensor q_out = qo ? *qo : empty(q.sizes(), q.scalar_type(), dev);
   const bsa_heads oq = heads(q_out, "q_out", true);
   const float eps = number(a[11]);
   const int inter = truth(a[12]);
@@ -493,7 +498,7 @@ PyObject* attend(PyObject* const* a) {
   const int iR = as_int(R, "block_table"), iT = as_int(T, "q"), iH = as_int(Hq, "q"), iW = as_int(width, "block_table");
   const size_t need = bsa_paged_attention_workspace_bytes(cache, iR, iT, iH, max_new, iW);
   if (need == 0) throw LibError{"bsa_paged_attention_workspace_bytes", BSA_ERR_UNSUPPORTED};
-  const at::Tensor out = po ? *po : at::empty(q.sizes(), q.options());
+  const at::Tensor out = po ? *po : empty(q.sizes(), q.scalar_type(), dev);
   const bsa_heads ho = heads(out, "out", true);
   const at::Tensor work = workspace_or_new(ws, need, dev);
   launch("bsa_paged_chunk_attention", dev, [&](void* st) {
