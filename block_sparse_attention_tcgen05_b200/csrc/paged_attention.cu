@@ -98,7 +98,6 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
 constexpr int kTokWarps = 4;
 constexpr int kTokThreads = 32 * kTokWarps;
 constexpr int kTokChunk = 64;     // keys of a work unit: one 16-key block per warp
-constexpr int kTokMinSpan = 4;    // units a CTA takes at least
 
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   uint4 r;
@@ -142,7 +141,7 @@ __device__ __forceinline__ int token_chunks(const PagedArgs& a, const Request& q
 // The unit space: request-major, then KV head, then chunk; CTA w takes [w*span, (w+1)*span).
 __device__ __forceinline__ int64_t token_span(int64_t units, int workers) {
   const int64_t s = (units + workers - 1) / workers;
-  return s < kTokMinSpan ? kTokMinSpan : s;
+  return s < 1 ? 1 : s;
 }
 
 // Partial results: two slots per CTA (0: a (request, head) that began before its span, 1: one
@@ -1308,7 +1307,7 @@ PagedPlan paged_plan(int R, int T, int Hq, int Hkv, int D, int max_new, int widt
   p.tile = most > kTokenRows;
   p.min_rows = p.token ? kTokenRows : 0;
   const int64_t keys = static_cast<int64_t>(width) * page;
-  p.one_each = keys <= kTokMinSpan * kTokChunk;
+  p.one_each = keys <= kTokChunk;  // nothing to share out
   p.workers = p.one_each ? R * Hkv : kTokCtas;
   size_t b = 0;
   if (p.token && !p.one_each)
