@@ -561,8 +561,8 @@ int check_norm_common(const bsa_shape& s, const void* qw, const void* kw, const 
   if (static_cast<int64_t>(s.B) * s.Sq * std::max(s.Hq, s.Hkv) > (int64_t(1) << 36))
     return fail(BSA_ERR_UNSUPPORTED, "more than 2^36 rows");
   if (!(eps >= 0.f)) return fail(BSA_ERR_INVALID_ARG, "eps < 0");
-  if (!qw || !kw || !cos || !sin) return fail(BSA_ERR_INVALID_ARG, "null pointer");
   if (n_pos < 0) return fail(BSA_ERR_INVALID_ARG, "n_pos < 0");
+  if (!qw || !kw || (n_pos > 0 && (!cos || !sin))) return fail(BSA_ERR_INVALID_ARG, "null pointer");
   if (reinterpret_cast<uintptr_t>(cos) % 16 || reinterpret_cast<uintptr_t>(sin) % 16)
     return fail(BSA_ERR_INVALID_ARG, "cos and sin must be 16-byte aligned");
   return BSA_OK;

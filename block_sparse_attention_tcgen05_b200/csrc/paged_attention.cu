@@ -136,6 +136,12 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
   return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
 }
 
+// Weight of a partial result (maximum m, sum l) under the joint maximum: 0 for one that saw no key,
+// NaN for one whose logits were all NaN (which no maximum shows).
+__device__ __forceinline__ float part_weight(float m, float l, float joint) {
+  return m == -INFINITY ? l : ex2(m - joint);
+}
+
 // Chunks of 64 keys of request r that the token kernel takes (0 for one of the tile kernel's).
 __device__ __forceinline__ int token_chunks(const PagedArgs& a, const Request& q) {
   if (q.n <= 0 || q.n * static_cast<int64_t>(a.G) > a.tok_rows) return 0;
@@ -436,15 +442,15 @@ __global__ void __launch_bounds__(kTokThreads) paged_token_kernel(const PagedArg
       float lt = 0.f, o0 = 0.f, o1 = 0.f;
 #pragma unroll
       for (int w = 0; w < kTokWarps; ++w) {
-        const float f = s_m[w][row] == -INFINITY ? 0.f : ex2(s_m[w][row] - mt);
+        const float f = part_weight(s_m[w][row], s_l[w][row], mt);
         lt = fmaf(s_l[w][row], f, lt);
-        if (f > 0.f) {
+        if (f != 0.f) {
           o0 = fmaf(s_o[w][row][d], f, o0);
           o1 = fmaf(s_o[w][row][d + 1], f, o1);
         }
       }
       if (whole) {
-        const float inv = lt > 0.f ? 1.f / lt : 0.f;
+        const float inv = lt == 0.f ? 0.f : 1.f / lt;
         T* po = static_cast<T*>(a.out) + (static_cast<int64_t>(h) * a.G + row % a.G) * a.oh +
                 static_cast<int64_t>(q.t0 + row / a.G) * a.ot + d;
         *reinterpret_cast<uint32_t*>(po) = pack_pair<T>(o0 * inv, o1 * inv);
@@ -517,7 +523,7 @@ __global__ void __launch_bounds__(32 * kCombWarps) token_combine_kernel(const Pa
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (ml[i].x == -INFINITY) continue;  // saw no key of this row
+      if (ml[i].x == -INFINITY && ml[i].y == 0.f) continue;  // saw no key of this row
       const float mn = fmaxf(mt, ml[i].x), f0 = ex2(mt - mn), f1 = ex2(ml[i].x - mn);
       lt = lt * f0 + ml[i].y * f1;
 #pragma unroll
@@ -540,12 +546,12 @@ __global__ void __launch_bounds__(32 * kCombWarps) token_combine_kernel(const Pa
     float l = 0.f, o0 = 0.f, o1 = 0.f;
 #pragma unroll
     for (int w = 0; w < kCombWarps; ++w) {
-      const float f = s_ml[w].x == -INFINITY ? 0.f : ex2(s_ml[w].x - m);
+      const float f = part_weight(s_ml[w].x, s_ml[w].y, m);
       l = fmaf(s_ml[w].y, f, l);
       o0 = fmaf(s_acc[w][2 * tid], f, o0);
       o1 = fmaf(s_acc[w][2 * tid + 1], f, o1);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     T* po = static_cast<T*>(a.out) + (static_cast<int64_t>(h) * a.G + row % a.G) * a.oh +
             static_cast<int64_t>(q.t0 + row / a.G) * a.ot;
     *reinterpret_cast<uint32_t*>(po + 2 * tid) = pack_pair<T>(o0 * inv, o1 * inv);
@@ -1158,7 +1164,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // Out through the tile's Q, which no product reads any more: each lane's half row in pieces of
     // 16 bytes (piece x of row r at x ^ r), then row by row. A warp has 32 rows of D bytes.
     constexpr int UH = D / 16;  // pieces of a row
-    const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+    const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
     uint8_t* stage = smem + t * Cfg::TILE + (warp & 7) * (Cfg::TILE / 8);
     const int uh = lane % UH;
     auto put = [&](int piece, const uint4& x) {
@@ -1205,7 +1211,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         take(p * 16, o);
         uint32_t w[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) w[c] = l_run > 0.f ? pack_pair<T>(o[2 * c] * inv, o[2 * c + 1] * inv) : 0u;
+        for (int c = 0; c < 8; ++c) w[c] = l_run == 0.f ? 0u : pack_pair<T>(o[2 * c] * inv, o[2 * c + 1] * inv);
         put(2 * p, make_uint4(w[0], w[1], w[2], w[3]));
         put(2 * p + 1, make_uint4(w[4], w[5], w[6], w[7]));
       }
@@ -1268,7 +1274,7 @@ __global__ void __launch_bounds__(kJoinThreads) tile_combine_kernel(const PagedA
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      if (x[i].x == -INFINITY) continue;  // a part that saw no key of this row
+      if (x[i].x == -INFINITY && x[i].y == 0.f) continue;  // a part that saw no key of this row
       const float mn = fmaxf(m[i], x[i].x), f0 = ex2(m[i] - mn), f1 = ex2(x[i].x - mn);
       sum[i] = sum[i] * f0 + x[i].y * f1;
       acc[i].x = acc[i].x * f0 + o[i].x * f1;
@@ -1282,7 +1288,7 @@ __global__ void __launch_bounds__(kJoinThreads) tile_combine_kernel(const PagedA
   for (int i = 0; i < kRows; ++i) {
     const int rr = rr0 + i * (32 / L);
     if (rr >= rows) continue;
-    const float inv = sum[i] > 0.f ? 1.f / sum[i] : 0.f;
+    const float inv = sum[i] == 0.f ? 0.f : 1.f / sum[i];
     const int row = job.tile * kTileRows + rr;
     T* po = static_cast<T*>(a.out) + (static_cast<int64_t>(h) * a.G + row % a.G) * a.oh +
             static_cast<int64_t>(q.t0 + row / a.G) * a.ot;

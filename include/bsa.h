@@ -518,6 +518,7 @@ int bsa_qk_norm_rotation(bsa_heads q, bsa_heads k, bsa_shape shape, const void* 
  *   dq, dk         : written. Rows of skipped positions (see above) get zeros.
  *   dq_weight, dk_weight : device float32 (D), written.
  *   workspace      : >= bsa_qk_norm_rotation_workspace_bytes(shape), 256-byte aligned.
+ * Limits of both calls: B*S < 2^31, at most 16384 heads a side, 2^36 rows.
  */
 size_t bsa_qk_norm_rotation_workspace_bytes(bsa_shape shape);
 int bsa_qk_norm_rotation_backward(bsa_heads dq_out, bsa_heads dk_out, bsa_heads q, bsa_heads k,
@@ -613,9 +614,11 @@ int bsa_paged_qk_norm_append(bsa_heads q, bsa_heads k, bsa_heads v, int T, int H
  *   scale     : <= 0 selects 1/sqrt(D). out: (Hq, T, D) of the cache's type, any strides.
  *   workspace : >= bsa_paged_attention_workspace_bytes(cache, R, T, Hq, max_new, width).
  * Rows of the cache behind a request's last token, and masked pages, are never read into a
- * result (they may hold NaN). A NaN or infinity in a value row that some token of a causal
+ * result (they may hold NaN). A row whose logits hold NaN, or +infinity, gets NaN. A NaN or infinity in a value row that some token of a causal
  * chunk sees may also reach tokens of the chunk that do not see it (their weight 0 times it). Hq a multiple of Hkv. fp32 logits, sums and accumulators; the
- * weights are rounded to the cache's type before the second product.
+ * weights are rounded to the cache's type before the second product. Limits: T * Hq <= 2^30, a
+ * block-table row of at most 2^28 keys, all of them together 2^36. A workspace belongs to one
+ * call at a time, replays of a graph that captured it included.
  */
 size_t bsa_paged_attention_workspace_bytes(bsa_paged_cache cache, int R, int T, int Hq,
                                            int max_new, int width);

@@ -183,6 +183,8 @@ def test_empty_and_graph_and_other_stream():
     q, k, qw, kw, cos, sin = _inputs(1, 4, 2, 33, 128, torch.bfloat16, "fused")
     e = bsa.qk_norm_rotation(q[:, :, :0], k[:, :, :0], qw, kw, cos, sin)
     assert e[0].shape == (1, 4, 0, 128)
+    none = bsa.qk_norm_rotation(q[:, :, :0], k[:, :, :0], qw, kw, cos[:0], sin[:0])
+    assert none[1].shape == (1, 2, 0, 128)
     g = bsa.qk_norm_rotation_backward(e[0], e[1], q[:, :, :0], k[:, :, :0], qw, kw, cos, sin)
     assert (g[2] == 0).all() and (g[3] == 0).all() and g[0].shape == (1, 4, 0, 128)
     want = bsa.qk_norm_rotation(q, k, qw, kw, cos, sin)

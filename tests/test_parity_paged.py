@@ -361,6 +361,50 @@ def test_an_invalid_page_counts_as_masked():
         _check(out, q, kc, vc, table, cu, ctx, True, mask)
 
 
+@pytest.mark.parametrize("n,ctx", [(1, 40), (1, 3000), (40, 100), (20, 2500)])
+def test_nan_and_infinite_queries_give_nan_in_their_rows_alone(n, ctx):
+    bsa = _bsa()
+    q, kc, vc, table, cu, _ = _attention_case(50, [ctx], [n], 4, 2, 64, 16, torch.bfloat16)
+    want = bsa.paged_chunk_attention(q, kc, vc, _i32(table), _i32(cu), _i32([ctx]), max_new=n)
+    q[1, 0, 3] = float("nan")
+    q[2, n - 1] = float("inf")
+    out = bsa.paged_chunk_attention(q, kc, vc, _i32(table), _i32(cu), _i32([ctx]), max_new=n)
+    assert torch.isnan(out[1, 0]).all() and torch.isnan(out[2, n - 1]).all()
+    ok = torch.ones(4, n, dtype=torch.bool)
+    ok[1, 0] = ok[2, n - 1] = False
+    assert torch.equal(out[:, :n][ok], want[:, :n][ok])
+
+
+def test_a_cache_past_32_bits_of_elements():
+    """Pages whose elements lie past 2^31 and 2^32 bytes into the pool, written and read by every
+    kernel."""
+    bsa = _bsa()
+    Hkv, page, D = 4, 64, 128
+    n_pages = (1 << 31) // (Hkv * page * D) + 40  # 4.3 GB
+    pool = torch.empty(n_pages, Hkv, page, D, dtype=torch.bfloat16, device=DEV)
+    values = torch.empty_like(pool)
+    g = torch.Generator().manual_seed(51)
+    pages = [n_pages - 1, 2, n_pages - 7, n_pages - 2, n_pages // 2 + 1]
+    small = torch.randn(5, Hkv, page, D, generator=g).to(torch.bfloat16).to(DEV)
+    for i, p in enumerate(pages):
+        pool[p] = small[i]
+    for n in (1, 50):
+        ctx = [5 * page - n]
+        q = torch.randn(8, n, D, generator=g).to(torch.bfloat16).to(DEV)
+        args = (_i32([0, n]), _i32(ctx))
+        far = bsa.paged_chunk_attention(q, pool, pool, _i32([pages]), *args, max_new=n)
+        near = bsa.paged_chunk_attention(q, small, small, _i32([[0, 1, 2, 3, 4]]), *args, max_new=n)
+        assert torch.equal(far, near)
+    x = torch.randn(4, 3 * 4, D, generator=g).to(torch.bfloat16).to(DEV)
+    w, cos, sin = torch.ones(D, device=DEV), torch.ones(9, 64, device=DEV), torch.zeros(9, 64, device=DEV)
+    slots = [pages[0] * page + 5, pages[2] * page, 7]
+    bsa.paged_qk_norm_append(x[:, :3], x[:, 3:6], x[:, 6:9], w, w, cos, sin, _i32([0, 1, 2]), _i32(slots), pool, values)
+    _, rk = bsa.qk_norm_rotation(x[None, :, :3], x[None, :, 3:6], w, w, cos, sin)
+    for t, (p, row) in enumerate(((pages[0], 5), (pages[2], 0), (0, 7))):
+        assert torch.equal(pool[p, :, row], rk[0, :, t]) and torch.equal(values[p, :, row], x[:, 6 + t])
+    assert bsa.device_status()[0] == 0
+
+
 def test_empty_calls():
     bsa = _bsa()
     kc = torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16, device=DEV)
