@@ -660,6 +660,16 @@ __device__ __forceinline__ bool find_tile(const PagedArgs& a, int u, int lane, T
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
     quantum = tile_quantum(a, work);
+    // Rounding up makes more jobs than the share allows for; where one wave is to do it all, the
+    // quantum grows until it does (40 pairs of 68 chunks: 120 jobs of 23 chunks, 64 us; as 160 jobs
+    // of 17 chunks, in two waves, 75).
+    if (a.R <= 32 && quantum < kTileLongShare) {
+      for (int i = 0; i < 4; ++i) {
+        const int jobs = __reduce_add_sync(0xffffffffu, pairs * tile_splits(chunks, quantum)) * a.Hkv;
+        if (jobs <= kTileSms || __all_sync(0xffffffffu, pairs == 0 || tile_splits(chunks, quantum) == 1)) break;
+        quantum = (quantum * jobs + kTileSms - 1) / kTileSms;
+      }
+    }
   }
   int base = 0, slots = 0;
   for (int r0 = 0; r0 < a.R; r0 += 32) {
@@ -1257,7 +1267,7 @@ __global__ void __launch_bounds__(kJoinThreads) tile_combine_kernel(const PagedA
     sum[i] = 0.f;
     acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-#pragma unroll 2
+#pragma unroll 4
   for (int s = 0; s < job.splits; ++s) {
     float2 x[kRows];
     float4 o[kRows];
