@@ -9,7 +9,9 @@ cache and the anti-diagonal block scoring + top-p selection at the video shape
 labels -> permutation -> gather -> centroid -> bitset stages and the fused
 compensated attention at the video-tile workload (245 clusters, nearest 22 % of tile
 pairs); probe selection, probe dense attention and the probe-fitted residual repair
-at the grouped-query shape (H=24 query heads over 8 KV heads, S=32768, M=64).
+at the grouped-query shape (H=24 query heads over 8 KV heads, S=32768, M=64); the
+per-head norm and rotation before them, forward and backward; and chunked generation over a
+paged cache (a frame of 30 x 52 tokens after 20 cached ones; single tokens).
 
 Timing: CUDA events on the launching stream, 5 warm-up calls, median of N calls
 (default 20), L2 flushed (a 256 MB write) before every timed call. Latency-class steps
@@ -302,13 +304,71 @@ def bench_probe_and_repair(timer, dev, hbm, tc, out):
                    3 * o.numel() * o.element_size(), "B", "hbm", hbm))
 
 
+def bench_heads_and_cache(timer, dev, hbm, tc, out):
+    """n1, n2: norms and rotation of a clip's heads, sliced from a fused projection, and their
+    gradients at the grouped-query shape. g1-g4: a frame's tables, append and attention over a
+    paged cache of the frames before it, and the attention of single tokens."""
+    g = torch.Generator(device=dev).manual_seed(6)
+
+    def randn(*shape):
+        return torch.randn(shape, generator=g, device=dev).to(torch.bfloat16)
+    S, w = 32768, torch.ones(D, device=dev)
+    ang = torch.rand(S, D // 2, generator=g, device=dev)
+    cos, sin = ang.cos(), ang.sin()
+    x = randn(1, 32760, 120, D).transpose(1, 2)
+    q, k = x[:, :40], x[:, 40:80]
+    ms = timer(lambda: ops.qk_norm_rotation(q, k, w, w, cos, sin))
+    out.append(row("n1", "per-head norm and rotation of q and k (40 + 40 heads, S=32760, from a "
+                   "fused projection)", ms, 4 * (q.numel() + k.numel()) + 2 * cos.numel() * 4, "B", "hbm", hbm))
+    del x, q, k
+    q, k = randn(1, S, 24, D).transpose(1, 2), randn(1, S, 8, D).transpose(1, 2)
+    dq, dk = randn(1, 24, S, D), randn(1, 8, S, D)
+    ms = timer(lambda: ops.qk_norm_rotation_backward(dq, dk, q, k, w, w, cos, sin))
+    out.append(row("n2", "its gradients (24 + 8 heads, S=32768)", ms,
+                   6 * (q.numel() + k.numel()) + 2 * cos.numel() * 4, "B", "hbm", hbm))
+    del q, k, dq, dk
+    frame, page, Hq, Hkv = 30 * 52, 64, 24, 8
+    ctx = 20 * frame
+    have, need = -(-ctx // page), -(-(ctx + frame) // page)
+    kc, vc = randn(need + 8, Hkv, page, D), randn(need + 8, Hkv, page, D)
+    order = torch.randperm(need + 8, generator=g, device=dev).to(torch.int32)
+    table = torch.full((1, need), -1, dtype=torch.int32, device=dev)
+    table[0, :have] = order[:have]
+    lens = [torch.tensor([n], dtype=torch.int32, device=dev) for n in (ctx, frame)]
+
+    def tables():
+        return ops.paged_block_tables(lens[0], lens[1], table, order[have:], frame, page, need + 8)
+    ms = timer(tables)
+    slots, pos, cu, _ = tables()
+    out.append(row("g1", "block table and slot map of a frame (1560 tokens)", ms, None, None, "latency", None))
+    out[-1]["ms_pipelined"] = timer.pipelined(tables)
+    x = randn(frame, Hq + 2 * Hkv, D).transpose(0, 1)
+    xq, xk, xv = x[:Hq], x[Hq:Hq + Hkv], x[Hq + Hkv:]
+
+    def append():
+        return ops.paged_qk_norm_append(xq, xk, xv, w, w, cos, sin, pos, slots, kc, vc)
+    ms = timer(append)
+    out.append(row("g2", "norm, rotation and cache append of the frame (24 + 8 heads)", ms, 4 * x.numel(), "B",
+                   "hbm", hbm))
+    q = append()
+    ms = timer(lambda: ops.paged_chunk_attention(q, kc, vc, table, cu, lens[0], causal=False, max_new=frame))
+    out.append(row("g3", "attention of the frame over 20 cached ones and itself (24 / 8 heads, 32760 keys)", ms,
+                   4.0 * D * frame * (ctx + frame) * Hq, "FLOP", "tensor", tc))
+    one = torch.tensor([0, 1], dtype=torch.int32, device=dev)
+    last = lens[0] + frame - 1
+    qt = q[:, :1].contiguous()
+    ms = timer(lambda: ops.paged_chunk_attention(qt, kc, vc, table, one, last, max_new=1))
+    out.append(row("g4", "attention of one token over 32760 keys (24 / 8 heads)", ms,
+                   4.0 * D * (ctx + frame) * Hkv, "B", "hbm", hbm))
+
+
 def main():
     p = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     p.add_argument("--calls", type=int, default=20)
     p.add_argument("--out", default=None, help="also write the JSON lines to this file")
     p.add_argument("--only", default=None,
                    help="comma-separated groups to run (cache_scoring, attention, routing, "
-                        "partition, probe_repair); default all")
+                        "partition, probe_repair, heads_and_cache); default all")
     args = p.parse_args()
     groups = set(args.only.split(",")) if args.only else None
     dev = torch.device("cuda", 0)
@@ -319,7 +379,8 @@ def main():
     t0 = time.time()
     for name, fn in (("cache_scoring", bench_cache_and_scoring), ("attention", bench_attention),
                      ("routing", bench_routing_and_sta), ("partition", bench_partition),
-                     ("probe_repair", bench_probe_and_repair)):
+                     ("probe_repair", bench_probe_and_repair),
+                     ("heads_and_cache", bench_heads_and_cache)):
         if groups is None or name in groups:
             fn(timer, dev, hbm, tc, out)
             torch.cuda.empty_cache()

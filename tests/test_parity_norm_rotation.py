@@ -202,3 +202,26 @@ def test_empty_and_graph_and_other_stream():
         graph.replay()
     st.synchronize()
     assert all(torch.equal(a, b) for a, b in zip((*want, *wantg), (*out, *grads)))
+
+
+def test_heads_from_a_fused_projection_go_into_block_sparse_attention():
+    """As a layer runs it: q and k normed and rotated out of the projection's slices, then the
+    block-sparse call on them, against the same arithmetic in float64 (attention tolerances of
+    its own parity tests)."""
+    import oracle
+    bsa = _bsa()
+    S, D, H, Hkv, C = 512, 64, 4, 2, 8
+    g = torch.Generator().manual_seed(9)
+    x = torch.randn(1, S, H + 2 * Hkv, D, generator=g).to(torch.bfloat16).to(DEV).transpose(1, 2)
+    q, k, v = x[:, :H], x[:, H:H + Hkv], x[:, H + Hkv:].contiguous()
+    _, _, qw, kw, cos, sin = _inputs(1, H, Hkv, S, D, torch.bfloat16, "heads")
+    qo, ko = bsa.qk_norm_rotation(q, k, qw, kw, cos, sin)
+    lab = (torch.arange(S) // 64).to(torch.int32)
+    mask = torch.rand(C, C, generator=g) < 0.4
+    mask |= torch.eye(C, dtype=torch.bool)
+    out = bsa.centroid_compensated_attention(qo, ko, v, lab.to(DEV), lab.to(DEV), mask.to(DEV))
+    rq, rk = (torch.tensor(nr.norm_rotation(_np(a), _np(w), _np(cos), _np(sin))).to(torch.bfloat16).double().numpy()
+              for a, w in ((q, qw), (k, kw)))
+    ref = oracle.centroid_compensated_attention(rq, rk, _np(v), lab.numpy(), lab.numpy(), mask.numpy())
+    err = np.abs(_np(out) - ref)
+    assert err.max() <= 2e-2 and np.linalg.norm(err) <= 5e-3 * np.linalg.norm(ref)
