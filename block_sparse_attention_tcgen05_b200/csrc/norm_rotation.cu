@@ -10,7 +10,10 @@
 // weights are read once per token and group.
 //
 // Everything is fp32 between the load and the one rounding of the store. The pass is bound
-// by HBM: each input row is read once, each output row written once.
+// by HBM: each input row is read once, each output row written once. 32760 tokens of 40 + 40
+// heads of 128 in bf16, out of a fused projection: 225 us, 92 % of the copy rate (loading rows
+// only when they are used, every head's pointer worked out anew: 326 us). The backward pass reads
+// a row more: 144 us for 32768 tokens of 24 + 8 heads, 86 %.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -574,7 +577,9 @@ HeadsOut out_of(const bsa_heads& h) { return {h.ptr, h.stride_b, h.stride_h, h.s
 // Heads of a run: a lane group walks over all heads of its token's section when the tokens
 // alone fill the GPU several times over, and over fewer, in whole steps of 4, when not.
 int heads_per_run(int64_t token_groups, int heads) {
-  constexpr int64_t kWant = 148 * 8;  // CTAs that give every SM its loads in flight
+  // CTAs to aim at. 1560 tokens into the cache: 13.3 us with 3, 4 or 6 per SM, 15.4 with 8;
+  // 4000 tokens of 80 heads: 44, 44, 36.9 and 37.9.
+  constexpr int64_t kWant = 148 * 6;
   const int64_t runs = std::min<int64_t>((heads + 3) / 4, std::max<int64_t>(1, kWant / std::max<int64_t>(token_groups, 1)));
   return static_cast<int>(((heads + runs - 1) / runs + 3) / 4 * 4);
 }

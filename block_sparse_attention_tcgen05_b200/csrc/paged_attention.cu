@@ -505,11 +505,12 @@ __global__ void __launch_bounds__(32 * kCombWarps) token_combine_kernel(const Pa
   const int64_t u0 = static_cast<int64_t>(before) * a.Hkv + static_cast<int64_t>(h) * nch;
   const int w0 = static_cast<int>(u0 / span), w1 = static_cast<int>((u0 + nch - 1) / span);
   if (w0 == w1) return;  // one CTA had all of it and wrote the result
+  constexpr int kAhead = 8;  // parts on their way to a warp
   float mt = -INFINITY, lt = 0.f, acc[D / 32] = {};
-  for (int w = w0 + warp; w <= w1; w += 4 * kCombWarps) {
-    float2 ml[4], v[4][D / 64];
+  for (int w = w0 + warp; w <= w1; w += kAhead * kCombWarps) {
+    float2 ml[kAhead], v[kAhead][D / 64];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kAhead; ++i) {
       const int wi = w + i * kCombWarps;
       ml[i] = make_float2(-INFINITY, 0.f);
 #pragma unroll
@@ -522,7 +523,7 @@ __global__ void __launch_bounds__(32 * kCombWarps) token_combine_kernel(const Pa
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kAhead; ++i) {
       if (ml[i].x == -INFINITY && ml[i].y == 0.f) continue;  // saw no key of this row
       const float mn = fmaxf(mt, ml[i].x), f0 = ex2(mt - mn), f1 = ex2(ml[i].x - mn);
       lt = lt * f0 + ml[i].y * f1;
