@@ -8,12 +8,20 @@
 //       that the matrix instruction takes, 16 keys at a time, with no shared memory on the
 //       way. The (request, head, 64-key chunk) space is cut into equal contiguous spans, one
 //       per CTA, so ragged lengths balance; a (request, head) that crosses a span border
-//       leaves partial results that token_combine_kernel joins.
+//       leaves partial results that token_combine_kernel joins. 64 requests of 11000 keys on
+//       average (24 / 8 heads of 128): 447 us, the cache's bytes at the measured copy rate; one
+//       request of 32761 keys: 31 us, floor 20 us, the rest is the way from the lengths over the
+//       pages to the first keys, and the join.
 //   paged_tile_kernel   more rows. tcgen05: two 128-row tiles per CTA over 128-key chunks
-//       gathered page by page with TMA, logits and weights in TMEM, one softmax thread per
-//       row. With few tiles the key range is split over CTAs and tile_combine_kernel joins.
+//       gathered page by page with TMA, logits and weights in TMEM, two softmax threads per
+//       row. Long requests are split over CTAs and tile_combine_kernel joins the parts. 1560
+//       rows of 40 heads over 32760 keys: 978 us in single calls (1070 TFLOP/s, 0.65 of the
+//       burst peak), 1.13 ms in calls without a pause, where the power limit lowers the
+//       clocks. Of a chunk's 3400 cycles the tensor core works 2600 and the exponentials take
+//       2050 of the special-function units; the rest is what passes between the two.
 //
-// Both keep the running maximum and sum of a softmax in fp32, in base-2 units.
+// Sums of a softmax are kept in fp32, in base-2 units: relative to a running maximum in the token
+// kernel, to a fixed reference in the tile kernel.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -835,400 +843,400 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     return pass == 1 || *redo == 0;
   };
   if (warp >= 16) {
-  // registers go from the last warpgroup to the softmax warpgroups
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    // registers go from the last warpgroup to the softmax warpgroups
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
 #pragma unroll 1
-  for (int pass = 0;; ++pass) {
-  if (warp == 17) {
-    // ------------------------------------------------ TMA warp: gathers chunks page by page
-    // A load takes lu = min(page, 128) rows; chunk = 128 / lu loads of kept pages, in order.
-    const int lu_shift = min(a.page_shift, 7), lu = 1 << lu_shift, per_chunk = 128 >> lu_shift;
-    const int32_t* trow = a.table + r * a.table_stride;
-    const uint8_t* mrow = a.mask ? a.mask + r * a.mr + h * a.mg : nullptr;
-    const int end = (key_hi + lu - 1) >> lu_shift;
-    // Lane i looks at load base + i of the request (its page, -1 where it is masked or behind the
-    // end); the next 32 are looked up while these are used.
-    auto look = [&](int base) -> int {
-      const int i = base + lane;
-      if (i >= end) return -1;
-      const int pg = static_cast<int>((static_cast<int64_t>(i) << lu_shift) >> a.page_shift);
-      const int id = trow[pg];
-      if (mrow && !mrow[pg]) return -1;
-      if (id < 0 || id >= a.n_pages) {
-        report_device_error(kStatusBadLabel, kPagedSite + 1);
-        return -1;
-      }
-      return id;
-    };
-    int base = key_lo >> lu_shift;
-    int id = look(base), id_next = look(base + 32);
-    unsigned left = __ballot_sync(0xffffffffu, id >= 0);
-    uint32_t loads = 0;   // stages filled so far
-    int tail_rows = 128;  // rows that hold keys in the last chunk (all in those before it)
-    bool ok = true;
-    for (int j = 0; ok; ++j) {
-      // (the record is free: the stage of the last chunk's keys was last used by the values of
-      // chunk j - 4, whose product waited for the softmax of that chunk)
-      TileInfo* ti = info + j % kTileInfo;
-      int filled = 0, last_i = -1;
-      while (filled < per_chunk && base < end) {
-        const int rank = filled + __popc(left & ((1u << lane) - 1u));
-        const bool take = ((left >> lane) & 1u) && rank < per_chunk;
-        if (take) {
-          ids[rank] = id;
-          for (int gk = 0; gk < lu / 16; ++gk) ti->pos[rank * (lu / 16) + gk] = ((base + lane) << lu_shift) + 16 * gk;
-        }
-        const unsigned taken = __ballot_sync(0xffffffffu, take);
-        filled += __popc(taken);
-        if (taken) last_i = base + 31 - __clz(taken);
-        left &= ~taken;
-        if (left == 0) {
-          base += 32;
-          id = id_next;
-          id_next = look(base + 32);
-          left = __ballot_sync(0xffffffffu, id >= 0);
-        }
-      }
-      const int granules = filled * (lu / 16);
-      if (lane < 8 && lane >= granules) ti->pos[lane] = kAbsent;
-      // rows that hold keys: all of the loads but what lies behind the last key that a row of
-      // the CTA sees
-      int valid = filled * lu;
-      if (filled) valid -= max(0, ((last_i + 1) << lu_shift) - key_end);
-      if (lane == 0) {
-        ti->rows = valid;
-        ti->last = valid == 128 ? (last_i << lu_shift) + lu - 1 : kAbsent;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(TBAR(TB_INFO + j % kTileInfo));
-      if (filled == 0) break;
-      tail_rows = valid;
+    for (int pass = 0;; ++pass) {
+      if (warp == 17) {
+        // ------------------------------------------------ TMA warp: gathers chunks page by page
+        // A load takes lu = min(page, 128) rows; chunk = 128 / lu loads of kept pages, in order.
+        const int lu_shift = min(a.page_shift, 7), lu = 1 << lu_shift, per_chunk = 128 >> lu_shift;
+        const int32_t* trow = a.table + r * a.table_stride;
+        const uint8_t* mrow = a.mask ? a.mask + r * a.mr + h * a.mg : nullptr;
+        const int end = (key_hi + lu - 1) >> lu_shift;
+        // Lane i looks at load base + i of the request (its page, -1 where it is masked or behind the
+        // end); the next 32 are looked up while these are used.
+        auto look = [&](int base) -> int {
+          const int i = base + lane;
+          if (i >= end) return -1;
+          const int pg = static_cast<int>((static_cast<int64_t>(i) << lu_shift) >> a.page_shift);
+          const int id = trow[pg];
+          if (mrow && !mrow[pg]) return -1;
+          if (id < 0 || id >= a.n_pages) {
+            report_device_error(kStatusBadLabel, kPagedSite + 1);
+            return -1;
+          }
+          return id;
+        };
+        int base = key_lo >> lu_shift;
+        int id = look(base), id_next = look(base + 32);
+        unsigned left = __ballot_sync(0xffffffffu, id >= 0);
+        uint32_t loads = 0;   // stages filled so far
+        int tail_rows = 128;  // rows that hold keys in the last chunk (all in those before it)
+        bool ok = true;
+        for (int j = 0; ok; ++j) {
+          // (the record is free: the stage of the last chunk's keys was last used by the values of
+          // chunk j - 4, whose product waited for the softmax of that chunk)
+          TileInfo* ti = info + j % kTileInfo;
+          int filled = 0, last_i = -1;
+          while (filled < per_chunk && base < end) {
+            const int rank = filled + __popc(left & ((1u << lane) - 1u));
+            const bool take = ((left >> lane) & 1u) && rank < per_chunk;
+            if (take) {
+              ids[rank] = id;
+              for (int gk = 0; gk < lu / 16; ++gk) ti->pos[rank * (lu / 16) + gk] = ((base + lane) << lu_shift) + 16 * gk;
+            }
+            const unsigned taken = __ballot_sync(0xffffffffu, take);
+            filled += __popc(taken);
+            if (taken) last_i = base + 31 - __clz(taken);
+            left &= ~taken;
+            if (left == 0) {
+              base += 32;
+              id = id_next;
+              id_next = look(base + 32);
+              left = __ballot_sync(0xffffffffu, id >= 0);
+            }
+          }
+          const int granules = filled * (lu / 16);
+          if (lane < 8 && lane >= granules) ti->pos[lane] = kAbsent;
+          // rows that hold keys: all of the loads but what lies behind the last key that a row of
+          // the CTA sees
+          int valid = filled * lu;
+          if (filled) valid -= max(0, ((last_i + 1) << lu_shift) - key_end);
+          if (lane == 0) {
+            ti->rows = valid;
+            ti->last = valid == 128 ? (last_i << lu_shift) + lu - 1 : kAbsent;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(TBAR(TB_INFO + j % kTileInfo));
+          if (filled == 0) break;
+          tail_rows = valid;
 #pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv) {
-        const uint32_t stage = loads % kTileStages;
-        if (loads >= kTileStages) {
-          ok = __all_sync(0xffffffffu, mbar_wait_poll(TBAR(TB_KV_EMPTY + stage), ((loads / kTileStages) - 1) & 1,
-                                                 abort_flag, kPagedSite + 11));
-          if (!ok) break;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(TBAR(TB_KV_FULL + stage), filled * lu * D * 2);
-        __syncwarp();
-        if (lane < filled) {
-          const int i_row = a.page_shift > 7 ? ti->pos[0] & ((1 << a.page_shift) - 1) : 0;
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t stage = loads % kTileStages;
+            if (loads >= kTileStages) {
+              ok = __all_sync(0xffffffffu, mbar_wait_poll(TBAR(TB_KV_EMPTY + stage), ((loads / kTileStages) - 1) & 1,
+                                                     abort_flag, kPagedSite + 11));
+              if (!ok) break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(TBAR(TB_KV_FULL + stage), filled * lu * D * 2);
+            __syncwarp();
+            if (lane < filled) {
+              const int i_row = a.page_shift > 7 ? ti->pos[0] & ((1 << a.page_shift) - 1) : 0;
 #pragma unroll
-          for (int cc = 0; cc < Cfg::NATOM; ++cc)
-            tma_load_4d(sKV + stage * Cfg::TILE + cc * 16384 + lane * lu * 128, kv ? &tmV : &tmK,
-                        TBAR(TB_KV_FULL + stage), cc * 64, i_row, h, ids[lane]);
-        }
-        __syncwarp();
-        ++loads;
-      }
-    }
-    // value rows without a key in the last chunk: zeros (what lies there may be anything, and
-    // 0 * NaN is NaN)
-    if (ok && tail_rows < 128) {
-      const uint32_t stage = (loads - 1) % kTileStages;
-      ok = wait_all(TBAR(TB_KV_FULL + stage), ((loads - 1) / kTileStages) & 1, kPagedSite + 13);
-      if (ok) {
-        for (int i = tail_rows * 8 + lane; i < 128 * 8; i += 32)
-#pragma unroll
-          for (int cc = 0; cc < Cfg::NATOM; ++cc)
-            *reinterpret_cast<uint4*>(smem + (2 + stage) * Cfg::TILE + cc * 16384 + i * 16) =
-                make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(TBAR(TB_TAIL));
-      }
-    }
-    // every copy has landed before the CTA may end
-    for (uint32_t i = loads > kTileStages ? loads - kTileStages : 0; i < loads; ++i)
-      mbar_wait_poll(TBAR(TB_KV_FULL + i % kTileStages), (i / kTileStages) & 1, never, kPagedSite + 12);
-  } else if (warp == 16 || (warp == 18 && two)) {
-    // ------------------------------------------------ MMA warps, one per tile
-    // The two halves of a chunk's keys are pipelines of their own: logits (and over them, their
-    // weights) in TMEM columns 128 t + 64 half, the output of both in columns 256 + 128 t. A
-    // half's next logits go where its weights were, QK(j + 1, half) right behind PV(j, half).
-    // So four pipelines (two tiles, two halves) keep the tensor core and the exponentials busy
-    // between them. A warp per tile, because a warp that has committed stands still until its
-    // products are done; the whole warp runs on uniform values, so that descriptors live in
-    // uniform registers (a lone thread took 75 cycles to issue a product that takes 64).
-    const int t = warp == 18 ? 1 : 0;
-    auto commit = [&](uint32_t bar) {
-      if (elect_one()) tc_commit(bar);
-      __syncwarp();
-    };
-    constexpr uint32_t kIdQK = make_idesc16(kF16, 128, 64, false, false);
-    constexpr uint32_t kIdPV = make_idesc16(kF16, 128, D, false, true);
-    const uint64_t dQ = smem_desc(sQ + t * Cfg::TILE, 16, 1024);
-    const uint64_t dKV = smem_desc(sKV, 16, 1024);
-    const uint64_t dV = smem_desc(sKV, 16384, 1024);
-    const uint32_t tS = tmem + 128 * t, tO = tmem + 256 + 128 * t;
-    auto issue_qk = [&](int half, uint32_t stage) {
-      const uint64_t kd = dKV + static_cast<uint64_t>((stage * Cfg::TILE + half * 64 * 128) >> 4);
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t off = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-          mma_ss<false>(tS + 64 * half, dQ + off, kd + off, kIdQK, kk > 0 ? 1u : 0u);
-        }
-      }
-      __syncwarp();
-    };
-    auto issue_pv = [&](int half, uint32_t stage, bool first) {
-      const uint64_t vd = dV + static_cast<uint64_t>((stage * Cfg::TILE + half * 4 * 2048) >> 4);
-      if (elect_one()) {
-#pragma unroll
-        for (int k4 = 0; k4 < 4; ++k4)
-          mma_ts<false>(tO, tS + 64 * half + k4 * 8, vd + static_cast<uint64_t>((k4 * 2048) >> 4), kIdPV,
-                        (!first || k4 > 0) ? 1u : 0u);
-      }
-      __syncwarp();
-    };
-    uint32_t vst = 1, kst = 2;  // stages of V(j) and K(j + 1)
-    bool ok = pass > 0 || wait_all(TBAR(TB_Q), 0, kPagedSite + 20);
-    ok = ok && wait_all(TBAR(TB_INFO), 0, kPagedSite + 21);
-    int rows_j = ok ? info[0].rows : 0;
-    if (ok && rows_j > 0 && (ok = wait_all(TBAR(TB_KV_FULL), 0, kPagedSite + 22))) {
-      tc_fence_after();
-      issue_qk(0, 0);
-      commit(TBAR(TB_S + 2 * t));
-      if (rows_j > 64) {
-        issue_qk(1, 0);
-        commit(TBAR(TB_S + 2 * t + 1));
-      }
-      commit(TBAR(TB_KV_EMPTY));
-    }
-    for (int j = 0; ok && rows_j > 0; ++j) {
-      // low half: its weights, V(j) and K(j + 1) are there
-      if (!(ok = wait_all(TBAR(TB_P + 2 * t), j & 1, kPagedSite + 25))) break;
-      tc_fence_after();
-      issue_pv(0, vst, j == 0);
-      const int next_rows = info[(j + 1) % kTileInfo].rows;
-      if (next_rows > 0) {
-        issue_qk(0, kst);
-        commit(TBAR(TB_S + 2 * t));
-      }
-      if (rows_j <= 64) break;     // (the last chunk)
-      // high half
-      if (!(ok = wait_all(TBAR(TB_P + 2 * t + 1), j & 1, kPagedSite + 28))) break;
-      tc_fence_after();
-      issue_pv(1, vst, false);
-      if (next_rows > 64) {
-        issue_qk(1, kst);
-        commit(TBAR(TB_S + 2 * t + 1));
-      }
-      commit(TBAR(TB_KV_EMPTY + vst));
-      if (next_rows > 0) commit(TBAR(TB_KV_EMPTY + kst));
-      rows_j = next_rows;
-      vst = vst + 2 >= kTileStages ? vst + 2 - kTileStages : vst + 2;
-      kst = kst + 2 >= kTileStages ? kst + 2 - kTileStages : kst + 2;
-    }
-    // every product has completed before the CTA may end
-    commit(TBAR(TB_DRAIN + t));
-    mbar_wait_poll(TBAR(TB_DRAIN + t), 0, never, kPagedSite + 27);
-  } else if (warp == 19) {
-    // ------------------------------------------------ stage warp
-    // A wait costs a warp 250 to 350 cycles here even when there is nothing to wait for, and the
-    // MMA warps' instructions are what a chunk's time consists of; so this warp waits for
-    // V(j), the next record and K(j + 1) in their place, and its arrival is one of those that
-    // complete the low half's weights.
-    uint32_t vst = 1, vph = 0, kst = 2, kph = 0;
-    bool ok = wait_all(TBAR(TB_INFO), 0, kPagedSite + 36);
-    int rows_j = ok ? info[0].rows : 0;
-    for (int j = 0; ok && rows_j > 0; ++j) {
-      if (!(ok = wait_all(TBAR(TB_KV_FULL + vst), vph, kPagedSite + 23))) break;
-      if (rows_j < 128 && !(ok = wait_all(TBAR(TB_TAIL), 0, kPagedSite + 35))) break;
-      if (!(ok = wait_all(TBAR(TB_INFO + (j + 1) % kTileInfo), ((j + 1) / kTileInfo) & 1, kPagedSite + 24))) break;
-      rows_j = info[(j + 1) % kTileInfo].rows;
-      if (rows_j > 0 && !(ok = wait_all(TBAR(TB_KV_FULL + kst), kph, kPagedSite + 26))) break;
-      if (j > 0) {  // one arrival in each phase
-        ok = wait_all(TBAR(TB_P), (j - 1) & 1, kPagedSite + 37);
-        if (ok && two) ok = wait_all(TBAR(TB_P + 2), (j - 1) & 1, kPagedSite + 37);
-        if (!ok) break;
-      }
-      if (lane == 0) {
-        mbar_arrive(TBAR(TB_P));
-        if (two) mbar_arrive(TBAR(TB_P + 2));
-      }
-      __syncwarp();
-      vst += 2;
-      if (vst >= kTileStages) { vst -= kTileStages; vph ^= 1u; }
-      kst += 2;
-      if (kst >= kTileStages) { kst -= kTileStages; kph ^= 1u; }
-    }
-  }
-  if (last_pass(pass)) break;
-  if (tid == 512) {
-    for (int i = 0; i < TB_COUNT; ++i) mbar_inval(TBAR(i));
-    init_barriers(two);
-  }
-  named_bar_sync(1, kTileThreads);
-  }
-  } else {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-#pragma unroll 1
-  for (int pass = 0;; ++pass) {
-    // ------------------------------------------------ softmax
-    const uint32_t tS = tmem + 128 * t + 64 * hb + lanes;  // this half's logits and weights
-    const uint32_t xbar = TBAR(TB_X + 4 * t + (warp & 3));
-    volatile float* xmine = s_max + (t * 2 + hb) * 128 + rr;
-    const volatile float* xother = s_max + (t * 2 + (hb ^ 1)) * 128 + rr;
-    if (pass == 0) {
-      // half of this warp's rows of Q into the swizzled tile (16-byte piece u of row r at u ^ (r & 7))
-      const T* src = static_cast<const T*>(a.q) + hq * a.qh + static_cast<int64_t>(q.t0 + tok) * a.qt;
-      uint4 v[UN / 2];
-#pragma unroll
-      for (int i = 0; i < UN / 2; ++i) {
-        const int r = hb * 16 + i * (32 / UN) + lane / UN;
-        const uint8_t* p = other_row(src, r) + 16 * u;
-        v[i] = 128 * t + (warp & 3) * 32 + r < rows ? ldg_stream(p) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int i = 0; i < UN / 2; ++i) {
-        const int r = (warp & 3) * 32 + hb * 16 + i * (32 / UN) + lane / UN;
-        *reinterpret_cast<uint4*>(smem + t * Cfg::TILE + (u >> 3) * 16384 + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = v[i];
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(TBAR(TB_Q));
-    }
-    const int lim = live ? (a.causal ? min(q.len - 1, q.ctx + tok) : q.len - 1) : -1;
-    // the smallest reach of the tile's rows (its first row's): chunks up to it need no mask
-    const int lim_tile = a.causal ? min(q.len - 1, q.ctx + (row0 + 128 * t) / a.G) : q.len - 1;
-    float seen = -INFINITY;  // largest logit (times the scale, base 2)
-    bool ok = t == 0 || two;
-    l_run = 0.f;
-    nch = 0;
-#pragma unroll 1
-    for (int j = 0; ok; ++j) {
-      if (!(ok = wait_all(TBAR(TB_INFO + j % kTileInfo), (j / kTileInfo) & 1, kPagedSite + 30))) break;
-      const TileInfo* ti = info + j % kTileInfo;
-      if (ti->rows == 0) break;
-      const bool edge = ti->last > lim_tile, has = ti->rows > 64 * hb;
-      ++nch;
-      float v[2][32];
-      if (has) {
-        if (!(ok = wait_all(TBAR(TB_S + 2 * t + hb), j & 1, kPagedSite + 31))) break;
-        tc_fence_after();
-        tmem_ld32(tS, v[0]);
-        tmem_ld32(tS + 32, v[1]);
-        tmem_wait_ld();
-        if (edge) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int vis = lim - ti->pos[4 * hb + i];  // last visible column of the granule
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-              if (c > vis) v[i >> 1][(i & 1) * 16 + c] = -INFINITY;
+              for (int cc = 0; cc < Cfg::NATOM; ++cc)
+                tma_load_4d(sKV + stage * Cfg::TILE + cc * 16384 + lane * lu * 128, kv ? &tmV : &tmK,
+                            TBAR(TB_KV_FULL + stage), cc * 64, i_row, h, ids[lane]);
+            }
+            __syncwarp();
+            ++loads;
           }
         }
-      }
-      if (j == 0 && pass == 0) {  // the reference, of both halves
-        *xmine = has ? max64(v[0], v[1]) * a.scale_log2 : -INFINITY;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(xbar);
-        if (!(ok = wait_all(xbar, 0, kPagedSite + 33))) break;
-        m_row = fmaxf(*xmine, *xother);
-      }
-      if (!has) break;  // (the last chunk)
-      const float neg = m_row == -INFINITY ? 0.f : -m_row;
-      float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f, q0 = -INFINITY, q1 = -INFINITY;
+        // value rows without a key in the last chunk: zeros (what lies there may be anything, and
+        // 0 * NaN is NaN)
+        if (ok && tail_rows < 128) {
+          const uint32_t stage = (loads - 1) % kTileStages;
+          ok = wait_all(TBAR(TB_KV_FULL + stage), ((loads - 1) / kTileStages) & 1, kPagedSite + 13);
+          if (ok) {
+            for (int i = tail_rows * 8 + lane; i < 128 * 8; i += 32)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t w[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          float x0, x1;
-          fma2(x0, x1, v[i][2 * c], v[i][2 * c + 1], a.scale_log2, a.scale_log2, neg, neg);
-          if (c & 1) q1 = max3(q1, x0, x1);
-          else q0 = max3(q0, x0, x1);
-          x0 = ex2(x0);
-          x1 = ex2(x1);
-          if (c & 1) add2(s2, s3, s2, s3, x0, x1);
-          else add2(s0, s1, s0, s1, x0, x1);
-          w[c] = pack_pair<T>(x0, x1);
+              for (int cc = 0; cc < Cfg::NATOM; ++cc)
+                *reinterpret_cast<uint4*>(smem + (2 + stage) * Cfg::TILE + cc * 16384 + i * 16) =
+                    make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(TBAR(TB_TAIL));
+          }
         }
-        tmem_st16(tS + 16 * i, w);
+        // every copy has landed before the CTA may end
+        for (uint32_t i = loads > kTileStages ? loads - kTileStages : 0; i < loads; ++i)
+          mbar_wait_poll(TBAR(TB_KV_FULL + i % kTileStages), (i / kTileStages) & 1, never, kPagedSite + 12);
+      } else if (warp == 16 || (warp == 18 && two)) {
+        // ------------------------------------------------ MMA warps, one per tile
+        // The two halves of a chunk's keys are pipelines of their own: logits (and over them, their
+        // weights) in TMEM columns 128 t + 64 half, the output of both in columns 256 + 128 t. A
+        // half's next logits go where its weights were, QK(j + 1, half) right behind PV(j, half).
+        // So four pipelines (two tiles, two halves) keep the tensor core and the exponentials busy
+        // between them. A warp per tile, because a warp that has committed stands still until its
+        // products are done; the whole warp runs on uniform values, so that descriptors live in
+        // uniform registers (a lone thread took 75 cycles to issue a product that takes 64).
+        const int t = warp == 18 ? 1 : 0;
+        auto commit = [&](uint32_t bar) {
+          if (elect_one()) tc_commit(bar);
+          __syncwarp();
+        };
+        constexpr uint32_t kIdQK = make_idesc16(kF16, 128, 64, false, false);
+        constexpr uint32_t kIdPV = make_idesc16(kF16, 128, D, false, true);
+        const uint64_t dQ = smem_desc(sQ + t * Cfg::TILE, 16, 1024);
+        const uint64_t dKV = smem_desc(sKV, 16, 1024);
+        const uint64_t dV = smem_desc(sKV, 16384, 1024);
+        const uint32_t tS = tmem + 128 * t, tO = tmem + 256 + 128 * t;
+        auto issue_qk = [&](int half, uint32_t stage) {
+          const uint64_t kd = dKV + static_cast<uint64_t>((stage * Cfg::TILE + half * 64 * 128) >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t off = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+              mma_ss<false>(tS + 64 * half, dQ + off, kd + off, kIdQK, kk > 0 ? 1u : 0u);
+            }
+          }
+          __syncwarp();
+        };
+        auto issue_pv = [&](int half, uint32_t stage, bool first) {
+          const uint64_t vd = dV + static_cast<uint64_t>((stage * Cfg::TILE + half * 4 * 2048) >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int k4 = 0; k4 < 4; ++k4)
+              mma_ts<false>(tO, tS + 64 * half + k4 * 8, vd + static_cast<uint64_t>((k4 * 2048) >> 4), kIdPV,
+                            (!first || k4 > 0) ? 1u : 0u);
+          }
+          __syncwarp();
+        };
+        uint32_t vst = 1, kst = 2;  // stages of V(j) and K(j + 1)
+        bool ok = pass > 0 || wait_all(TBAR(TB_Q), 0, kPagedSite + 20);
+        ok = ok && wait_all(TBAR(TB_INFO), 0, kPagedSite + 21);
+        int rows_j = ok ? info[0].rows : 0;
+        if (ok && rows_j > 0 && (ok = wait_all(TBAR(TB_KV_FULL), 0, kPagedSite + 22))) {
+          tc_fence_after();
+          issue_qk(0, 0);
+          commit(TBAR(TB_S + 2 * t));
+          if (rows_j > 64) {
+            issue_qk(1, 0);
+            commit(TBAR(TB_S + 2 * t + 1));
+          }
+          commit(TBAR(TB_KV_EMPTY));
+        }
+        for (int j = 0; ok && rows_j > 0; ++j) {
+          // low half: its weights, V(j) and K(j + 1) are there
+          if (!(ok = wait_all(TBAR(TB_P + 2 * t), j & 1, kPagedSite + 25))) break;
+          tc_fence_after();
+          issue_pv(0, vst, j == 0);
+          const int next_rows = info[(j + 1) % kTileInfo].rows;
+          if (next_rows > 0) {
+            issue_qk(0, kst);
+            commit(TBAR(TB_S + 2 * t));
+          }
+          if (rows_j <= 64) break;     // (the last chunk)
+          // high half
+          if (!(ok = wait_all(TBAR(TB_P + 2 * t + 1), j & 1, kPagedSite + 28))) break;
+          tc_fence_after();
+          issue_pv(1, vst, false);
+          if (next_rows > 64) {
+            issue_qk(1, kst);
+            commit(TBAR(TB_S + 2 * t + 1));
+          }
+          commit(TBAR(TB_KV_EMPTY + vst));
+          if (next_rows > 0) commit(TBAR(TB_KV_EMPTY + kst));
+          rows_j = next_rows;
+          vst = vst + 2 >= kTileStages ? vst + 2 - kTileStages : vst + 2;
+          kst = kst + 2 >= kTileStages ? kst + 2 - kTileStages : kst + 2;
+        }
+        // every product has completed before the CTA may end
+        commit(TBAR(TB_DRAIN + t));
+        mbar_wait_poll(TBAR(TB_DRAIN + t), 0, never, kPagedSite + 27);
+      } else if (warp == 19) {
+        // ------------------------------------------------ stage warp
+        // A wait costs a warp 250 to 350 cycles here even when there is nothing to wait for, and the
+        // MMA warps' instructions are what a chunk's time consists of; so this warp waits for
+        // V(j), the next record and K(j + 1) in their place, and its arrival is one of those that
+        // complete the low half's weights.
+        uint32_t vst = 1, vph = 0, kst = 2, kph = 0;
+        bool ok = wait_all(TBAR(TB_INFO), 0, kPagedSite + 36);
+        int rows_j = ok ? info[0].rows : 0;
+        for (int j = 0; ok && rows_j > 0; ++j) {
+          if (!(ok = wait_all(TBAR(TB_KV_FULL + vst), vph, kPagedSite + 23))) break;
+          if (rows_j < 128 && !(ok = wait_all(TBAR(TB_TAIL), 0, kPagedSite + 35))) break;
+          if (!(ok = wait_all(TBAR(TB_INFO + (j + 1) % kTileInfo), ((j + 1) / kTileInfo) & 1, kPagedSite + 24))) break;
+          rows_j = info[(j + 1) % kTileInfo].rows;
+          if (rows_j > 0 && !(ok = wait_all(TBAR(TB_KV_FULL + kst), kph, kPagedSite + 26))) break;
+          if (j > 0) {  // one arrival in each phase
+            ok = wait_all(TBAR(TB_P), (j - 1) & 1, kPagedSite + 37);
+            if (ok && two) ok = wait_all(TBAR(TB_P + 2), (j - 1) & 1, kPagedSite + 37);
+            if (!ok) break;
+          }
+          if (lane == 0) {
+            mbar_arrive(TBAR(TB_P));
+            if (two) mbar_arrive(TBAR(TB_P + 2));
+          }
+          __syncwarp();
+          vst += 2;
+          if (vst >= kTileStages) { vst -= kTileStages; vph ^= 1u; }
+          kst += 2;
+          if (kst >= kTileStages) { kst -= kTileStages; kph ^= 1u; }
+        }
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(TBAR(TB_P + 2 * t + hb));
-      l_run += (s0 + s1) + (s2 + s3);
-      seen = max3(seen, q0, q1);  // relative to the row's reference
+      if (last_pass(pass)) break;
+      if (tid == 512) {
+        for (int i = 0; i < TB_COUNT; ++i) mbar_inval(TBAR(i));
+        init_barriers(two);
+      }
+      named_bar_sync(1, kTileThreads);
     }
-    ok_all = ok || !(t == 0 || two);
-    // A row that the reference is too low for: its largest logit of all goes to both halves.
-    if (__any_sync(0xffffffffu, seen > kExcess) && lane == 0) *redo = 1;
-    *xmine = seen;
-    if (last_pass(pass)) break;
-    const float most = fmaxf(seen, *xother);
-    if (m_row > -INFINITY) m_row += fmaxf(most, 0.f);
-    named_bar_sync(1, kTileThreads);
-  }
-  // (every product and copy has ended) the sums of a row's halves, through the first stage
-  volatile float* sums = reinterpret_cast<volatile float*>(smem + 2 * Cfg::TILE);
-  sums[(t * 2 + hb) * 128 + rr] = l_run;
-  named_bar_sync(2, 512);
-  if (ok_all && (t == 0 || two)) {
-    l_run = sums[t * 256 + rr] + sums[t * 256 + 128 + rr];
-    // Out through the tile's Q, which no product reads any more: each lane's half row in pieces of
-    // 16 bytes (piece x of row r at x ^ r), then row by row. A warp has 32 rows of D bytes.
-    constexpr int UH = D / 16;  // pieces of a row
-    const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-    uint8_t* stage = smem + t * Cfg::TILE + (warp & 7) * (Cfg::TILE / 8);
-    const int uh = lane % UH;
-    auto put = [&](int piece, const uint4& x) {
-      *reinterpret_cast<uint4*>(stage + lane * D + ((piece ^ (lane & (UH - 1))) << 4)) = x;
-    };
-    auto drain = [&](void* row_ptr) {
-      __syncwarp();
-#pragma unroll 4
-      for (int i = 0; i < UH; ++i) {
-        const int r = i * (32 / UH) + lane / UH;
-        uint8_t* p = other_row(row_ptr, r);
-        const uint4 x = *reinterpret_cast<const uint4*>(stage + r * D + ((uh ^ (r & (UH - 1))) << 4));
-        if (128 * t + (warp & 3) * 32 + r < rows) *reinterpret_cast<uint4*>(p + 16 * uh) = x;
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+#pragma unroll 1
+    for (int pass = 0;; ++pass) {
+      // ------------------------------------------------ softmax
+      const uint32_t tS = tmem + 128 * t + 64 * hb + lanes;  // this half's logits and weights
+      const uint32_t xbar = TBAR(TB_X + 4 * t + (warp & 3));
+      volatile float* xmine = s_max + (t * 2 + hb) * 128 + rr;
+      const volatile float* xother = s_max + (t * 2 + (hb ^ 1)) * 128 + rr;
+      if (pass == 0) {
+        // half of this warp's rows of Q into the swizzled tile (16-byte piece u of row r at u ^ (r & 7))
+        const T* src = static_cast<const T*>(a.q) + hq * a.qh + static_cast<int64_t>(q.t0 + tok) * a.qt;
+        uint4 v[UN / 2];
+#pragma unroll
+        for (int i = 0; i < UN / 2; ++i) {
+          const int r = hb * 16 + i * (32 / UN) + lane / UN;
+          const uint8_t* p = other_row(src, r) + 16 * u;
+          v[i] = 128 * t + (warp & 3) * 32 + r < rows ? ldg_stream(p) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < UN / 2; ++i) {
+          const int r = (warp & 3) * 32 + hb * 16 + i * (32 / UN) + lane / UN;
+          *reinterpret_cast<uint4*>(smem + t * Cfg::TILE + (u >> 3) * 16384 + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = v[i];
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(TBAR(TB_Q));
       }
-      __syncwarp();
-    };
-    auto take = [&](int col, float(&o)[16]) {
-      if (nch > 0) {
-        tmem_ld16(tO + col, o);
-        tmem_wait_ld();
+      const int lim = live ? (a.causal ? min(q.len - 1, q.ctx + tok) : q.len - 1) : -1;
+      // the smallest reach of the tile's rows (its first row's): chunks up to it need no mask
+      const int lim_tile = a.causal ? min(q.len - 1, q.ctx + (row0 + 128 * t) / a.G) : q.len - 1;
+      float seen = -INFINITY;  // largest logit (times the scale, base 2)
+      bool ok = t == 0 || two;
+      l_run = 0.f;
+      nch = 0;
+#pragma unroll 1
+      for (int j = 0; ok; ++j) {
+        if (!(ok = wait_all(TBAR(TB_INFO + j % kTileInfo), (j / kTileInfo) & 1, kPagedSite + 30))) break;
+        const TileInfo* ti = info + j % kTileInfo;
+        if (ti->rows == 0) break;
+        const bool edge = ti->last > lim_tile, has = ti->rows > 64 * hb;
+        ++nch;
+        float v[2][32];
+        if (has) {
+          if (!(ok = wait_all(TBAR(TB_S + 2 * t + hb), j & 1, kPagedSite + 31))) break;
+          tc_fence_after();
+          tmem_ld32(tS, v[0]);
+          tmem_ld32(tS + 32, v[1]);
+          tmem_wait_ld();
+          if (edge) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int vis = lim - ti->pos[4 * hb + i];  // last visible column of the granule
+#pragma unroll
+              for (int c = 0; c < 16; ++c)
+                if (c > vis) v[i >> 1][(i & 1) * 16 + c] = -INFINITY;
+            }
+          }
+        }
+        if (j == 0 && pass == 0) {  // the reference, of both halves
+          *xmine = has ? max64(v[0], v[1]) * a.scale_log2 : -INFINITY;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(xbar);
+          if (!(ok = wait_all(xbar, 0, kPagedSite + 33))) break;
+          m_row = fmaxf(*xmine, *xother);
+        }
+        if (!has) break;  // (the last chunk)
+        const float neg = m_row == -INFINITY ? 0.f : -m_row;
+        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f, q0 = -INFINITY, q1 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t w[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            float x0, x1;
+            fma2(x0, x1, v[i][2 * c], v[i][2 * c + 1], a.scale_log2, a.scale_log2, neg, neg);
+            if (c & 1) q1 = max3(q1, x0, x1);
+            else q0 = max3(q0, x0, x1);
+            x0 = ex2(x0);
+            x1 = ex2(x1);
+            if (c & 1) add2(s2, s3, s2, s3, x0, x1);
+            else add2(s0, s1, s0, s1, x0, x1);
+            w[c] = pack_pair<T>(x0, x1);
+          }
+          tmem_st16(tS + 16 * i, w);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(TBAR(TB_P + 2 * t + hb));
+        l_run += (s0 + s1) + (s2 + s3);
+        seen = max3(seen, q0, q1);  // relative to the row's reference
+      }
+      ok_all = ok || !(t == 0 || two);
+      // A row that the reference is too low for: its largest logit of all goes to both halves.
+      if (__any_sync(0xffffffffu, seen > kExcess) && lane == 0) *redo = 1;
+      *xmine = seen;
+      if (last_pass(pass)) break;
+      const float most = fmaxf(seen, *xother);
+      if (m_row > -INFINITY) m_row += fmaxf(most, 0.f);
+      named_bar_sync(1, kTileThreads);
+    }
+    // (every product and copy has ended) the sums of a row's halves, through the first stage
+    volatile float* sums = reinterpret_cast<volatile float*>(smem + 2 * Cfg::TILE);
+    sums[(t * 2 + hb) * 128 + rr] = l_run;
+    named_bar_sync(2, 512);
+    if (ok_all && (t == 0 || two)) {
+      l_run = sums[t * 256 + rr] + sums[t * 256 + 128 + rr];
+      // Out through the tile's Q, which no product reads any more: each lane's half row in pieces of
+      // 16 bytes (piece x of row r at x ^ r), then row by row. A warp has 32 rows of D bytes.
+      constexpr int UH = D / 16;  // pieces of a row
+      const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+      uint8_t* stage = smem + t * Cfg::TILE + (warp & 7) * (Cfg::TILE / 8);
+      const int uh = lane % UH;
+      auto put = [&](int piece, const uint4& x) {
+        *reinterpret_cast<uint4*>(stage + lane * D + ((piece ^ (lane & (UH - 1))) << 4)) = x;
+      };
+      auto drain = [&](void* row_ptr) {
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < UH; ++i) {
+          const int r = i * (32 / UH) + lane / UH;
+          uint8_t* p = other_row(row_ptr, r);
+          const uint4 x = *reinterpret_cast<const uint4*>(stage + r * D + ((uh ^ (r & (UH - 1))) << 4));
+          if (128 * t + (warp & 3) * 32 + r < rows) *reinterpret_cast<uint4*>(p + 16 * uh) = x;
+        }
+        __syncwarp();
+      };
+      auto take = [&](int col, float(&o)[16]) {
+        if (nch > 0) {
+          tmem_ld16(tO + col, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) o[c] = 0.f;
+        }
+      };
+      if (splits > 1) {  // unnormalised fp32, D bytes of a row at a time
+        const size_t prow = tile_part_row(a, where->slot + split, h, 128 * t + rr);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int p = 0; p < D / 64; ++p) {
+            float o[16];
+            take(half * (D / 4) + p * 16, o);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) put(4 * p + c, *reinterpret_cast<uint4*>(o + 4 * c));
+          }
+          drain(a.part + prow * D + hb * (D / 2) + half * (D / 4));
+        }
+        if (live && hb == 0) *reinterpret_cast<float2*>(tile_part_ml(a, D) + prow * 2) = make_float2(m_row, l_run);
       } else {
 #pragma unroll
-        for (int c = 0; c < 16; ++c) o[c] = 0.f;
-      }
-    };
-    if (splits > 1) {  // unnormalised fp32, D bytes of a row at a time
-      const size_t prow = tile_part_row(a, where->slot + split, h, 128 * t + rr);
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-#pragma unroll
-        for (int p = 0; p < D / 64; ++p) {
+        for (int p = 0; p < D / 32; ++p) {
           float o[16];
-          take(half * (D / 4) + p * 16, o);
+          take(p * 16, o);
+          uint32_t w[8];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) put(4 * p + c, *reinterpret_cast<uint4*>(o + 4 * c));
+          for (int c = 0; c < 8; ++c) w[c] = l_run == 0.f ? 0u : pack_pair<T>(o[2 * c] * inv, o[2 * c + 1] * inv);
+          put(2 * p, make_uint4(w[0], w[1], w[2], w[3]));
+          put(2 * p + 1, make_uint4(w[4], w[5], w[6], w[7]));
         }
-        drain(a.part + prow * D + hb * (D / 2) + half * (D / 4));
+        drain(static_cast<T*>(a.out) + hq * a.oh + static_cast<int64_t>(q.t0 + tok) * a.ot + hb * (D / 2));
       }
-      if (live && hb == 0) *reinterpret_cast<float2*>(tile_part_ml(a, D) + prow * 2) = make_float2(m_row, l_run);
-    } else {
-#pragma unroll
-      for (int p = 0; p < D / 32; ++p) {
-        float o[16];
-        take(p * 16, o);
-        uint32_t w[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) w[c] = l_run == 0.f ? 0u : pack_pair<T>(o[2 * c] * inv, o[2 * c + 1] * inv);
-        put(2 * p, make_uint4(w[0], w[1], w[2], w[3]));
-        put(2 * p + 1, make_uint4(w[4], w[5], w[6], w[7]));
-      }
-      drain(static_cast<T*>(a.out) + hq * a.oh + static_cast<int64_t>(q.t0 + tok) * a.ot + hb * (D / 2));
     }
-  }
   }
 #undef TBAR
   tc_fence_before();
