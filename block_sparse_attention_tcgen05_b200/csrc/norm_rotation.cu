@@ -20,7 +20,7 @@
 #include <algorithm>
 
 #include "common.cuh"
-#include "ptx.cuh"
+#include "ptx_paged.cuh"
 
 namespace bsa {
 
