@@ -256,10 +256,14 @@ template <class F>
 void launch(const char* fn, c10::Device dev, F&& f) {
   c10::cuda::CUDAGuard guard(dev);
   void* stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
-  int st;
-  Py_BEGIN_ALLOW_THREADS
-  st = f(stream);
-  Py_END_ALLOW_THREADS
+  struct WithoutGil {  // taken back also when f throws
+    PyThreadState* state = PyEval_SaveThread();
+    ~WithoutGil() { PyEval_RestoreThread(state); }
+  };
+  const int st = [&] {
+    WithoutGil g;
+    return f(stream);
+  }();
   if (st != BSA_OK) throw LibError{fn, st};
 }
 

@@ -709,6 +709,8 @@ int bsa_qk_norm_rotation_backward(bsa_heads dq_out, bsa_heads dk_out, bsa_heads 
   if (!workspace || workspace_bytes < bsa_qk_norm_rotation_workspace_bytes(shape))
     return fail(BSA_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes,
                 bsa_qk_norm_rotation_workspace_bytes(shape));
+  if (reinterpret_cast<uintptr_t>(workspace) % 256)
+    return fail(BSA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   NormBackArgs a{};
   a.x[0] = in_of(q);
   a.x[1] = in_of(k);

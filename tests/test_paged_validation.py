@@ -142,6 +142,9 @@ def test_c_abi_refusals(lib):
                                              fake, fake, fake, 8, null) == _lib.BSA_ERR_WORKSPACE
     assert lib.bsa_qk_norm_rotation_backward(h, h, h, h, sh, fake, fake, 1, fake, fake, 8, null, 0, 1e-6, 1, h, h,
                                              null, fake, fake, 1 << 20, null) == _lib.BSA_ERR_INVALID_ARG
+    odd = ctypes.c_void_p((1 << 20) + 16)
+    assert lib.bsa_qk_norm_rotation_backward(h, h, h, h, sh, fake, fake, 1, fake, fake, 8, null, 0, 1e-6, 1, h, h,
+                                             fake, fake, odd, 1 << 20, null) == _lib.BSA_ERR_INVALID_ARG
 
     def tables(R=2, page=16, n_pages=9, T=4, stride=3, cu=fake):
         return lib.bsa_paged_block_tables(fake, fake, R, fake, 3, stride, fake, 2, T, page, n_pages, fake, fake,
@@ -159,6 +162,7 @@ def test_c_abi_refusals(lib):
     assert attend(_cache(stride=68)) == attend(_cache(k=0)) == attend(_cache(k=(1 << 20) + 8)) == -1
     assert attend(Hq=3) == attend(max_new=-1) == attend(q=bad_h) == attend(q=no_h) == -1
     assert attend(ws=null) == attend(nbytes=64) == _lib.BSA_ERR_WORKSPACE
+    assert attend(ws=odd) == -1
     assert attend(T=0) == attend(R=0) == attend(max_new=0) == 0
     assert lib.bsa_paged_attention_workspace_bytes(_cache(), 2, 4, 4, 1, 3) > 0
     assert lib.bsa_paged_attention_workspace_bytes(_cache(D=96), 2, 4, 4, 1, 3) == 0
