@@ -1,9 +1,10 @@
 """Training-free block-sparse attention for video DiTs on NVIDIA B200 (sm_100a).
 
 The compute path lives in ``libbsa.so`` (hand-written CUDA for sm_100a behind a C ABI,
-declared in ``include/bsa.h``). This package is its thin Python binding: it checks
-arguments, allocates outputs and workspaces with torch and calls the library on the
-current CUDA stream. It has no CPU fallback; a missing library raises.
+declared in ``include/bsa.h``). This package is its thin Python binding (ctypes, and a native
+module for the calls that run down to single tokens): it checks arguments, allocates outputs
+and workspaces with torch and calls the library on the current CUDA stream. It has no CPU
+fallback; a missing library raises.
 """
 
 from ._lib import BsaError, load as load_library  # noqa: F401

@@ -1167,11 +1167,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       ok_all = ok || !(t == 0 || two);
       // A row that the reference is too low for: its largest logit of all goes to both halves.
-      if (__any_sync(0xffffffffu, seen > kExcess) && lane == 0) *redo = 1;
+      // So it does where the first chunk gave no reference (all its logits -infinity).
+      const bool low = seen > kExcess || (m_row == -INFINITY && seen > -INFINITY);
+      if (__any_sync(0xffffffffu, live && low) && lane == 0) *redo = 1;
       *xmine = seen;
       if (last_pass(pass)) break;
       const float most = fmaxf(seen, *xother);
-      if (m_row > -INFINITY) m_row += fmaxf(most, 0.f);
+      m_row = m_row > -INFINITY ? m_row + fmaxf(most, 0.f) : most;
       named_bar_sync(1, kTileThreads);
     }
     // (every product and copy has ended) the sums of a row's halves, through the first stage

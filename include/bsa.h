@@ -611,12 +611,16 @@ int bsa_paged_qk_norm_append(bsa_heads q, bsa_heads k, bsa_heads v, int T, int H
  *               they were.
  *   page_mask : device uint8, element (r, g, page index in the request) at
  *               r*mask_r_stride + g*mask_g_stride + index; NULL keeps every page.
- *   scale     : <= 0 selects 1/sqrt(D). out: (Hq, T, D) of the cache's type, any strides.
+ *   scale     : <= 0 selects 1/sqrt(D). out: (Hq, T, D) of the cache's type, any strides; it
+ *               may be q itself (same pointer and strides), but may not overlap it otherwise.
  *   workspace : >= bsa_paged_attention_workspace_bytes(cache, R, T, Hq, max_new, width).
  * Rows of the cache behind a request's last token, and masked pages, are never read into a
- * result (they may hold NaN). A row whose logits hold NaN, or +infinity, gets NaN. A NaN or infinity in a value row that some token of a causal
- * chunk sees may also reach tokens of the chunk that do not see it (their weight 0 times it). Hq a multiple of Hkv. fp32 logits, sums and accumulators; the
- * weights are rounded to the cache's type before the second product. Limits: T * Hq <= 2^30, a
+ * result (they may hold NaN). A row whose logits hold NaN, or +infinity, gets
+ * NaN. A NaN or infinity in a value row that some token of a causal chunk sees may also reach
+ * tokens of the chunk that do not see it (their weight 0 times it). Hq a multiple of Hkv. fp32
+ * logits, sums and accumulators; the weights, up to 2^60 before the sum divides them (bf16; fp16
+ * 2^14), are rounded to the cache's type before the second product: values of magnitude up to
+ * 2^39 cannot overflow. Limits: T * Hq <= 2^30, a
  * block-table row of at most 2^28 keys, all of them together 2^36. A workspace belongs to one
  * call at a time, replays of a graph that captured it included.
  */

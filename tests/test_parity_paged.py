@@ -287,6 +287,39 @@ def test_chunks_whose_logits_rise(dt, D, ctx, new, causal):
     _check(out, q, kc, vc, table, cu, ctx, causal, None)
 
 
+@pytest.mark.parametrize("ctx,n", [(600, 40), (2300, 20), (600, 1)])
+@pytest.mark.parametrize("dt,D", [("bf16", 128), ("f16", 64)])
+def test_first_keys_at_minus_infinity(dt, D, ctx, n):
+    """The first 128 keys' logits are all -infinity (their weight is 0); the later ones are far
+    above 0 in some rows and far below in others."""
+    bsa = _bsa()
+    q, kc, vc, table, cu, _ = _attention_case(45, [ctx], [n], 2, 1, D, 64, TYPES[dt], None, 1.0, False, True)
+    used = table[0]
+    q[1] *= 40.0
+    kc[..., 0] = 0.0
+    q[0, :, 0], q[1, :, 0] = 60.0, 0.5
+    kc[used[2:], :, :, 0] = torch.where(torch.isnan(kc[used[2:], :, :, 1]), float("nan"), -40.0).to(kc.dtype)
+    kc[used[:2], :, :, 0] = float("-inf")
+    out = bsa.paged_chunk_attention(q, kc, vc, _i32(table), _i32(cu), _i32([ctx]), causal=True, max_new=n)
+    assert bsa.device_status() == (0, 0)
+    mask = np.ones((1, 1, len(used)), dtype=bool)
+    mask[..., :2] = False
+    clean = kc.clone()
+    clean[used[:2]] = 0.0
+    _check(out, q, clean, vc, table, cu, [ctx], True, mask)
+
+
+@pytest.mark.parametrize("ctx,n", [([600, 30], [40, 3]), ([9000], [1]), ([2300], [20])])
+def test_output_in_place_of_the_queries(ctx, n):
+    bsa = _bsa()
+    q, kc, vc, table, cu, _ = _attention_case(46, ctx, n, 4, 2, 128, 16, torch.bfloat16)
+    args = (kc, vc, _i32(table), _i32(cu), _i32(ctx))
+    want = bsa.paged_chunk_attention(q, *args, max_new=max(n))
+    got = bsa.paged_chunk_attention(q, *args, max_new=max(n), out=q)
+    assert got is q or got.data_ptr() == q.data_ptr()
+    assert torch.equal(got[:, :cu[-1]], want[:, :cu[-1]])
+
+
 def test_chunks_split_keys():
     _run([2500], [20], 2, 1, 128, 64, "bf16", True, seed=5, gain=3.0)
     _run([4200], [9], 2, 1, 64, 16, "f16", False, seed=6)
