@@ -59,6 +59,7 @@ struct PagedArgs {
   float* part;
   int tile_ctas;   // tile kernel: CTAs per KV head (a bound: those past the last one end at once)
   int can_split;   // tile kernel: 0 when no request is long enough to be split
+  int heads_first; // tile kernel: neighbouring CTAs take one job of all KV heads
   int workers;     // token kernel: CTAs
   int tok_rows;    // token kernel: rows of a request that its instance holds (8 or 16)
   int one_each;    // token kernel: one CTA per (request, KV head), nothing to join
@@ -642,8 +643,10 @@ __device__ __forceinline__ int tile_splits(int chunks, int64_t quantum) {
   return 4 * static_cast<int64_t>(chunks) <= 5 * quantum ? 1 : static_cast<int>((chunks + quantum - 1) / quantum);
 }
 
-// Job u of a KV head (by one warp, 32 requests at a time); with kJoin, the u-th pair that is
-// split. False past the last one.
+// CTA u's job of a KV head (by one warp, 32 requests at a time); with kJoin, the u-th pair that
+// is split. False where there is none. Causal tiles near the end of a request see the most keys,
+// so the last jobs go to the first CTAs. With heads first the CTAs without a job come last, except
+// in calls of more than 32 requests, where counting the jobs would read the lengths once more.
 template <bool kJoin>
 __device__ __forceinline__ bool find_tile(const PagedArgs& a, int u, int lane, TileJob* job) {
   int pairs = 0, chunks = 0;  // of the lane's request of a round
@@ -679,6 +682,11 @@ __device__ __forceinline__ bool find_tile(const PagedArgs& a, int u, int lane, T
         quantum = (quantum * jobs + kTileSms - 1) / kTileSms;
       }
     }
+  }
+  if (!kJoin) {
+    const int jobs = a.heads_first && a.R <= 32 ? __reduce_add_sync(0xffffffffu, pairs * tile_splits(chunks, quantum)) : a.tile_ctas;
+    u = jobs - 1 - u;
+    if (u < 0) return false;
   }
   int base = 0, slots = 0;
   for (int r0 = 0; r0 < a.R; r0 += 32) {
@@ -747,7 +755,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #define TBAR(i) (bar0 + 8u * static_cast<uint32_t>(i))
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.y;
+  const int h = a.heads_first ? blockIdx.x : blockIdx.y;
   auto init_barriers = [&](bool both) {
     for (int i = 0; i < TB_COUNT; ++i) {
       uint32_t n = 1;
@@ -762,8 +770,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   if (warp == 0) {
     TileJob job{};
-    // causal tiles near the end of a request see the most keys: they start first
-    const bool found = find_tile<false>(a, a.tile_ctas - 1 - static_cast<int>(blockIdx.x), lane, &job);
+    const bool found = find_tile<false>(a, a.heads_first ? blockIdx.y : blockIdx.x, lane, &job);
     if (lane == 0) {
       if (!found) job.r = -1;
       *where = job;
@@ -1323,12 +1330,19 @@ struct PagedPlan {
   bool token, tile;  // which kernels run
   int min_rows;      // rows up to which a request is the token kernel's
   int workers, one_each;
-  int tile_ctas, can_split, join_pairs;
+  int tile_ctas, can_split, join_pairs, heads_first;
   size_t bytes;
   size_t tile_off;
 };
 
 constexpr int kTokCtas = 148 * 6;
+
+// With heads first the longest jobs of all heads start first and the CTAs without a job are the
+// grid's last; with a head after the other, the CTAs at work share a head's keys. The first is
+// faster while all the keys and values fit L2: 7 chunks of up to 600 rows x 16 heads of 64 with two
+// pages of five kept, over up to 12000 keys (92 MB): 92 us and 100; 16000 keys (120 MB): 100 and 96;
+// 1560 rows of 40 heads over 32760 keys: 1047 and 980.
+constexpr int64_t kHeadsFirstBytes = int64_t(96) << 20;
 
 PagedPlan paged_plan(int R, int T, int Hq, int Hkv, int D, int max_new, int width, int page) {
   PagedPlan p{};
@@ -1350,6 +1364,7 @@ PagedPlan paged_plan(int R, int T, int Hq, int Hkv, int D, int max_new, int widt
     const int64_t pairs = static_cast<int64_t>(T) * G / kTileRows + std::min(R, T);
     p.can_split = keys > kTileMinChunks * 128;
     p.tile_ctas = static_cast<int>(pairs + (p.can_split ? ceil_div(kTileJobs, Hkv) : 0));
+    p.heads_first = keys * R * Hkv * D * 4 <= kHeadsFirstBytes && p.tile_ctas < 65536;  // (grid.y)
     p.join_pairs = static_cast<int>(std::min<int64_t>(pairs, ceil_div(kTileJobs, Hkv)));
     if (p.can_split) b += align_up(static_cast<size_t>(kTileSlots) * kTileRows * (D + 2) * sizeof(float), 256);
   }
@@ -1406,6 +1421,7 @@ int launch_paged(PagedArgs a, const PagedPlan& p, const bsa_paged_cache& c, char
     t.min_rows = p.min_rows;
     t.tile_ctas = p.tile_ctas;
     t.can_split = p.can_split;
+    t.heads_first = p.heads_first;
     CUtensorMap mk, mv;
     const CUtensorMapDataType dt = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -1423,7 +1439,7 @@ int launch_paged(PagedArgs a, const PagedPlan& p, const bsa_paged_cache& c, char
     e = check_cuda(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         TileCfg<D>::SMEM_LAUNCH), "cudaFuncSetAttribute(paged_tile_kernel)");
     if (e != BSA_OK) return e;
-    const dim3 grid(p.tile_ctas, a.Hkv);
+    const dim3 grid(p.heads_first ? a.Hkv : p.tile_ctas, p.heads_first ? p.tile_ctas : a.Hkv);
     // After the token kernel's join it starts at once: it shares neither rows nor workspace with it.
     if (p.token) {
       e = check_cuda(launch_dependent(kern, grid, dim3(kTileThreads), TileCfg<D>::SMEM_LAUNCH, st, mk, mv, t),

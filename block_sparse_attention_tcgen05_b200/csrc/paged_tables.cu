@@ -4,7 +4,8 @@
 // 4096 of them, read from L2) and then writes its own run of tokens, so no CTA waits for
 // another. A new page's table entry is written by the thread of the first token in it; the
 // page number itself comes from the free list, never from the table entry that another CTA
-// may be writing. Bound by launch and latency: 8 bytes are written per token.
+// may be writing. Bound by launch and latency, 8 bytes being written per token: 256 requests of
+// 204000 new tokens 8.0 us a call, one token 6.9.
 #include <algorithm>
 
 #include "common.cuh"

@@ -320,6 +320,22 @@ def test_output_in_place_of_the_queries(ctx, n):
     assert torch.equal(got[:, :cu[-1]], want[:, :cu[-1]])
 
 
+@pytest.mark.parametrize("R", [3, 40])
+def test_a_wide_block_table_changes_nothing(R):
+    """A table much wider than the requests (the order of the work depends on its reach)."""
+    bsa = _bsa()
+    rng = np.random.default_rng(47)
+    ctx, new = list(rng.integers(0, 2300, R)), list(rng.integers(0, 90, R))
+    ctx[0], new[0] = 2300, 300
+    q, kc, vc, table, cu, _ = _attention_case(47, ctx, new, 4, 2, 64, 32, torch.float16)
+    wide = np.full((R, 16384), -1)
+    wide[:, :table.shape[1]] = table
+    got = [bsa.paged_chunk_attention(q, kc, vc, _i32(t), _i32(cu), _i32(ctx), max_new=300)[:, :cu[-1]]
+           for t in (table, wide)]
+    assert bsa.device_status() == (0, 0) and torch.equal(*got)
+    _check(got[1], q[:, :cu[-1]], kc, vc, table, cu, ctx, True, None)
+
+
 def test_chunks_split_keys():
     _run([2500], [20], 2, 1, 128, 64, "bf16", True, seed=5, gain=3.0)
     _run([4200], [9], 2, 1, 64, 16, "f16", False, seed=6)
