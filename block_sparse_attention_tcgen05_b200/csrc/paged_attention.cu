@@ -955,6 +955,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (lane == 0) mbar_arrive(TBAR(TB_TAIL));
           }
         }
+        __syncwarp();
+        if (lane == 0) ids[0] = static_cast<int>(loads);  // (no page is looked up any more)
         // every copy has landed before the CTA may end
         for (uint32_t i = loads > kTileStages ? loads - kTileStages : 0; i < loads; ++i)
           mbar_wait_poll(TBAR(TB_KV_FULL + i % kTileStages), (i / kTileStages) & 1, never, kPagedSite + 12);
@@ -1023,7 +1025,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             issue_qk(0, kst);
             commit(TBAR(TB_S + 2 * t));
           }
-          if (rows_j <= 64) break;     // (the last chunk)
+          if (rows_j <= 64) {  // (the last chunk)
+            commit(TBAR(TB_KV_EMPTY + vst));
+            break;
+          }
           // high half
           if (!(ok = wait_all(TBAR(TB_P + 2 * t + 1), j & 1, kPagedSite + 28))) break;
           tc_fence_after();
@@ -1074,6 +1079,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       if (last_pass(pass)) break;
       if (tid == 512) {
+        // every stage's last release has arrived, before its barrier starts anew
+        const int loads = ids[0];
+        for (int s = 0; s < kTileStages && s < loads; ++s)
+          mbar_wait_poll(TBAR(TB_KV_EMPTY + s), ((loads - s - 1) / kTileStages) & 1, abort_flag, kPagedSite + 14);
         for (int i = 0; i < TB_COUNT; ++i) mbar_inval(TBAR(i));
         init_barriers(two);
       }
