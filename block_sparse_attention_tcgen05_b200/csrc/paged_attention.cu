@@ -1186,8 +1186,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // So it does where the first chunk gave no reference (all its logits -infinity).
       const bool low = seen > kExcess || (m_row == -INFINITY && seen > -INFINITY);
       if (__any_sync(0xffffffffu, live && low) && lane == 0) *redo = 1;
-      *xmine = seen;
       if (last_pass(pass)) break;
+      // The words that held the halves' first maxima serve again only here: every thread of the CTA
+      // has passed the barrier, so both halves have taken their references from them.
+      *xmine = seen;
+      named_bar_sync(2, 512);  // the softmax warps
       const float most = fmaxf(seen, *xother);
       m_row = m_row > -INFINITY ? m_row + fmaxf(most, 0.f) : most;
       named_bar_sync(1, kTileThreads);
