@@ -497,7 +497,10 @@ PyObject* attend(PyObject* const* a) {
   const bsa_heads hq = heads(q, "q");
   const c10::Device dev = same_device({&q, &kc, &vc, &bt, &cu, &ctx, mask, po, ws});
   const int causal = truth(a[6]);
-  const int max_new = a[7] == Py_None ? as_int(T, "q") : integer32(a[7], "max_new");
+  // A bound of 0 counts as 1: the library would return without looking at the lengths, and the
+  // rows of a request that has tokens all the same would stay uninitialised, unrecorded.
+  int max_new = a[7] == Py_None ? as_int(T, "q") : integer32(a[7], "max_new");
+  if (max_new == 0) max_new = 1;
   const float scale = number(a[9]);
   const int iR = as_int(R, "block_table"), iT = as_int(T, "q"), iH = as_int(Hq, "q"), iW = as_int(width, "block_table");
   const size_t need = bsa_paged_attention_workspace_bytes(cache, iR, iT, iH, max_new, iW);

@@ -1337,6 +1337,19 @@ __global__ void __launch_bounds__(kJoinThreads) tile_combine_kernel(const PagedA
   }
 }
 
+// A block table without columns: no key is left for any token, so their rows get 0 (grid: tokens),
+// and every request that has tokens is recorded, as one that passes its table.
+constexpr int kNoKeysThreads = 128;
+__global__ void __launch_bounds__(kNoKeysThreads) paged_no_keys_kernel(const PagedArgs a, int D) {
+  if (blockIdx.x == 0)
+    for (int r = threadIdx.x; r < a.R; r += kNoKeysThreads) check_request(a, r);
+  const int t = blockIdx.x, pieces = D / 8;  // of 16 bytes
+  if (t < a.cu[0] || t >= a.cu[a.R]) return;
+  for (int e = threadIdx.x; e < a.Hkv * a.G * pieces; e += kNoKeysThreads)
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + static_cast<int64_t>(e / pieces) * a.oh +
+                              static_cast<int64_t>(t) * a.ot + 8 * (e % pieces)) = make_uint4(0, 0, 0, 0);
+}
+
 // ================================================================ host side
 struct PagedPlan {
   bool token, tile;  // which kernels run
@@ -1493,8 +1506,8 @@ int bsa_paged_chunk_attention(bsa_heads q, bsa_paged_cache cache, const int32_t*
   using namespace bsa;
   int st = check_paged_sizes(cache, R, T, Hq, max_new, width);
   if (st != BSA_OK) return st;
-  if (R == 0 || T == 0 || max_new == 0 || width == 0) return BSA_OK;
-  if (!block_table || !cu_new || !context_lens || !q.ptr || !out.ptr)
+  if (R == 0 || T == 0 || max_new == 0) return BSA_OK;
+  if ((width > 0 && !block_table) || !cu_new || !context_lens || !q.ptr || !out.ptr)
     return fail(BSA_ERR_INVALID_ARG, "null pointer");
   if (reinterpret_cast<uintptr_t>(q.ptr) % 16 || reinterpret_cast<uintptr_t>(out.ptr) % 16 ||
       q.stride_h % 8 || q.stride_s % 8 || out.stride_h % 8 || out.stride_s % 8)
@@ -1540,6 +1553,11 @@ int bsa_paged_chunk_attention(bsa_heads q, bsa_paged_cache cache, const int32_t*
   a.max_new = max_new;
   char* ws = static_cast<char*>(workspace);
   cudaStream_t cs = as_stream(stream);
+  if (width == 0) {
+    paged_no_keys_kernel<<<T, kNoKeysThreads, 0, cs>>>(a, cache.D);
+    count_launch();
+    return check_cuda(cudaGetLastError(), "paged_no_keys_kernel");
+  }
   if (cache.dtype == BSA_F16)
     return cache.D == 64 ? launch_paged<__half, 64>(a, p, cache, ws, cs)
                          : launch_paged<__half, 128>(a, p, cache, ws, cs);

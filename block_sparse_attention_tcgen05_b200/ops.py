@@ -534,7 +534,7 @@ def paged_attention_workspace_bytes(q, k_cache, block_table, max_new=None):
     cache = _lib.PagedCache(256, 256, n, page, Hkv, D, _DT_PAGED[k_cache.dtype])
     R, width = block_table.shape
     return _lib.load().bsa_paged_attention_workspace_bytes(
-        cache, R, q.shape[1], q.shape[0], q.shape[1] if max_new is None else int(max_new), width)
+        cache, R, q.shape[1], q.shape[0], q.shape[1] if max_new is None else int(max_new) or 1, width)
 
 
 def paged_chunk_attention(q, k_cache, v_cache, block_table, cu_new, context_lens, causal=True,
@@ -543,7 +543,9 @@ def paged_chunk_attention(q, k_cache, v_cache, block_table, cu_new, context_lens
     before): q (Hq,T,D) packed by ``cu_new`` (int32 (R+1,)), caches (n_pages, Hkv, page, D)
     with pages of 16 to 256 tokens, ``block_table`` int32 (R, width), ``context_lens`` int32
     (R,). ``causal``: token i of a request sees the keys up to itself, else all of them.
-    ``max_new`` bounds the requests' new tokens (default T; 1 for a step of single tokens).
+    ``max_new`` bounds the requests' new tokens (default T; 1 for a step of single tokens, and
+    0 counts as 1); a request with more, or with keys past its row of the table, is recorded in
+    the device status.
     ``page_mask`` bool/uint8 (R, width) or (R, Hkv, width) keeps the pages that are not zero,
     shared by a KV head's query heads; a row that no key is left for gets 0. bf16 or fp16,
     D in {64, 128}. Returns q's type (Hq,T,D); rows from ``cu_new[R]`` on are not written."""

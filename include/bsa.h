@@ -602,13 +602,16 @@ int bsa_paged_qk_norm_append(bsa_heads q, bsa_heads k, bsa_heads v, int T, int H
  *   out = sum_j softmax_j(scale q . k_j) v_j        (a row that no key is left for gets 0)
  *   q         : device (Hq, T, D) of the cache's type, packed (stride_b not read).
  *   block_table : device int32, row r at r*table_stride, `width` entries. A page outside
- *               [0, n_pages) counts as masked and records BSA_ERR_INVALID_ARG.
+ *               [0, n_pages) counts as masked and records BSA_ERR_INVALID_ARG, and so do a
+ *               request's keys that lie past its row: with width 0 (block_table may be NULL)
+ *               the rows of all tokens get 0.
  *   cu_new    : device int32 (R + 1): request r's tokens are [cu_new[r], cu_new[r+1]).
  *               Rows from cu_new[R] on are left as they were. R <= 4096.
  *   context_lens : device int32 (R).
  *   max_new   : host bound of the requests' new tokens (1 for a step of single tokens); a
  *               request with more records BSA_ERR_INVALID_ARG and its rows may be left as
- *               they were.
+ *               they were. 0 says that no request has any: the call returns BSA_OK without a
+ *               launch, so nothing is written and no length is looked at.
  *   page_mask : device uint8, element (r, g, page index in the request) at
  *               r*mask_r_stride + g*mask_g_stride + index; NULL keeps every page.
  *   scale     : <= 0 selects 1/sqrt(D). out: (Hq, T, D) of the cache's type, any strides; it

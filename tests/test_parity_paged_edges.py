@@ -32,3 +32,40 @@ def test_few_chunks_whose_halves_differ(D, page, keep):
     again = [run() for _ in range(200)]
     torch.cuda.synchronize()
     assert all(torch.equal(first, x) for x in again)
+
+
+@pytest.mark.parametrize("new,want", [([2, 0, 1], -1), ([0, 0, 0], 0)])
+@pytest.mark.parametrize("dt,D", [(torch.bfloat16, 128), (torch.float16, 64)])
+def test_a_block_table_without_columns(dt, D, new, want):
+    """No key is left for any token: zeros, and an error for each request that has tokens."""
+    bsa = _bsa()
+    kc = torch.full((2, 2, 16, D), float("nan"), dtype=dt, device=DEV)
+    q = torch.ones(6, 5, D, dtype=dt, device=DEV)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    for layout in ("heads", "tokens"):
+        out = torch.full((6, 5, D) if layout == "heads" else (5, 6, D), 7.0, dtype=dt, device=DEV)
+        out = out if layout == "heads" else out.transpose(0, 1)
+        bsa.paged_chunk_attention(q, kc, kc, _i32(np.zeros((3, 0))), _i32(cu), _i32([0, 4, 0]), out=out)
+        assert bsa.device_status()[0] == want
+        assert (out[:, :cu[-1]] == 0).all() and (out[:, cu[-1]:] == 7.0).all()
+    mask = torch.ones(3, 2, 0, dtype=torch.bool, device=DEV)
+    out = bsa.paged_chunk_attention(q, kc, kc, _i32(np.zeros((3, 0))), _i32([-3, 2, 900, 1 << 30]), _i32([0] * 3),
+                                    page_mask=mask)
+    assert bsa.device_status()[0] == -1 and (out == 0).all()
+
+
+def test_a_bound_of_no_new_tokens():
+    """max_new = 0: a request of one token gets its row, one of more is recorded, and without
+    tokens nothing is written."""
+    bsa = _bsa()
+    q, kc, vc, table, cu, _ = _attention_case(61, [40, 7], [1, 1], 4, 2, 64, 16, torch.bfloat16)
+    args = (q, kc, vc, _i32(table))
+    ws = torch.empty(bsa.paged_attention_workspace_bytes(q, kc, _i32(table), 0), dtype=torch.uint8, device=DEV)
+    got = bsa.paged_chunk_attention(*args, _i32(cu), _i32([40, 7]), max_new=0, workspace=ws)
+    want = bsa.paged_chunk_attention(*args, _i32(cu), _i32([40, 7]), max_new=1)
+    assert bsa.device_status()[0] == 0 and torch.equal(got[:, :2], want[:, :2])
+    bsa.paged_chunk_attention(*args, _i32([0, 1, 3]), _i32([40, 6]), max_new=0)
+    assert bsa.device_status()[0] == -1
+    out = torch.full_like(q, 7.0)
+    bsa.paged_chunk_attention(*args, _i32([0, 0, 0]), _i32([40, 6]), max_new=0, out=out)
+    assert bsa.device_status()[0] == 0 and (out == 7.0).all()
