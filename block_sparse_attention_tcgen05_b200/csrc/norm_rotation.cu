@@ -475,7 +475,8 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rotation_back_kernel(con
           fma2(d0, d1, tb[i], tb[i + 1], wb[i], wb[i + 1], d0, d1);
         }
         const float ss = row_sum<D>(p0 + p1), dot = row_sum<D>(d0 + d1);
-        const float r = live ? rsqrtf(ss * (1.f / D) + a.eps) : 0.f;
+        // (a row behind the run's last head is zeros, whose root without an eps is infinite)
+        const float r = live && h0 + j < h_end ? rsqrtf(ss * (1.f / D) + a.eps) : 0.f;
         const float nk = -(r * r * dot * (1.f / D)) * r;
         float oa[4], ob[4];
 #pragma unroll
