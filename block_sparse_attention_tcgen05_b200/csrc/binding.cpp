@@ -9,6 +9,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -275,10 +276,25 @@ PyObject* wrap(std::initializer_list<at::Tensor> ts) {
   return r;
 }
 
+// Whether autograd is to record a call on these tensors.
+bool wants_grad(std::initializer_list<const at::Tensor*> ts) {
+  return c10::GradMode::is_enabled() &&
+         std::any_of(ts.begin(), ts.end(), [](const at::Tensor* t) { return t && t->requires_grad(); });
+}
+
+// (q_out, k_out), or None where autograd is to record the call: then the caller goes through its
+// autograd function, which calls again with gradients off.
 PyObject* norm(PyObject* const* a) {
   const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &qw = tensor(a[2], "q_weight"),
                    &kw = tensor(a[3], "k_weight"), &cos = tensor(a[4], "cos"), &sin = tensor(a[5], "sin");
   const at::Tensor *pos = optional(a[6], "positions"), *qo = optional(a[9], "q_out"), *ko = optional(a[10], "k_out");
+  if (wants_grad({&q, &k, &qw, &kw, &cos, &sin, qo, ko})) {
+    if (cos.requires_grad() || sin.requires_grad()) bad("cos, sin: no gradient is computed for the rotation");
+    if (qo || ko)
+      bad("q_out, k_out: given outputs are written outside autograd, but a tensor of the call requires a gradient "
+          "(leave them out, or call it under torch.no_grad())");
+    Py_RETURN_NONE;
+  }
   const Norm n = expect_norm(q, k, qw, kw, cos, sin, pos);
   if (qo) {
     expect_type(*qo, "q_out", {q.scalar_type()});

@@ -478,6 +478,33 @@ class MaskCache:
 # library call) is native: csrc/binding.cpp.
 
 
+def _as_heads(t):
+    """A (B,H,S,D) gradient as the library reads it: rows contiguous, everything else a multiple
+    of 16 bytes. Autograd hands over any strides (a sum's gradient is one number broadcast)."""
+    unit = 16 // t.element_size()
+    fits = t.stride(3) == 1 and t.data_ptr() % 16 == 0 and all(
+        t.stride(i) % unit == 0 for i in range(3) if t.shape[i] > 1)
+    return t if fits or t.numel() == 0 else t.clone(memory_format=torch.contiguous_format)
+
+
+class _QkNormRotation(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
+        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
+        ctx.options = eps, interleaved
+        return _lib.native().qk_norm_rotation(q, k, q_weight, k_weight, cos, sin, positions, eps,
+                                              interleaved, None, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        q, k, q_weight, k_weight, cos, sin, positions = ctx.saved_tensors
+        dq, dk, dqw, dkw = _lib.native().qk_norm_rotation_backward(
+            _as_heads(dq_out), _as_heads(dk_out), q, k, q_weight, k_weight, cos, sin, positions,
+            *ctx.options, None)
+        return dq, dk, dqw.to(q_weight.dtype), dkw.to(k_weight.dtype), *(None,) * 5
+
+
 def qk_norm_rotation(q, k, q_weight, k_weight, cos, sin, positions=None, eps=1e-6,
                      interleaved=True, q_out=None, k_out=None):
     """Per-head RMS norm and position rotation of q (B,Hq,S,D) and k (B,Hkv,S,D) in one
@@ -487,9 +514,13 @@ def qk_norm_rotation(q, k, q_weight, k_weight, cos, sin, positions=None, eps=1e-
     0..S-1. Pairs (2i, 2i+1), or (i, i + D/2) with ``interleaved=False``. Returns
     contiguous (q_out, k_out), or writes the given ones (any strides; q and k themselves are
     allowed). Rows of a position outside the table are left as they were (-1 marks padding,
-    another one is recorded in the device status)."""
-    return _lib.native().qk_norm_rotation(q, k, q_weight, k_weight, cos, sin, positions, eps,
-                                          interleaved, q_out, k_out)
+    another one is recorded in the device status). Autograd records the call, with
+    ``qk_norm_rotation_backward`` as its gradient; given outputs are refused then."""
+    out = _lib.native().qk_norm_rotation(q, k, q_weight, k_weight, cos, sin, positions, eps,
+                                         interleaved, q_out, k_out)
+    if out is None:  # a tensor of the call requires a gradient
+        out = _QkNormRotation.apply(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+    return out
 
 
 def qk_norm_rotation_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, positions=None,
@@ -498,7 +529,8 @@ def qk_norm_rotation_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin
     of its outputs (q's type, any strides, broadcast ones too) and its inputs. dq and dk are
     laid out as q and k are (token-major or contiguous); the weight gradients are fp32, summed
     over batch, heads and tokens in a fixed order. Rows that the forward call skips get
-    zero gradients."""
+    zero gradients. (Autograd calls it by itself; the other calls of this package return
+    tensors without a gradient.)"""
     return _lib.native().qk_norm_rotation_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos,
                                                    sin, positions, eps, interleaved, workspace)
 
