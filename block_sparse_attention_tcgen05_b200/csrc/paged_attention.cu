@@ -1423,11 +1423,10 @@ int launch_paged(PagedArgs a, const PagedPlan& p, const bsa_paged_cache& c, char
     const int64_t most = static_cast<int64_t>(std::min(a.max_new, a.T)) * a.G;
     t.tok_rows = most <= 8 ? 8 : kTokenRows;
     auto kern = most <= 8 ? paged_token_kernel<T, D, 1> : paged_token_kernel<T, D, 2>;
-    if (smem > 8192) {  // with the static part past the 48 KB that need no opt-in
-      const int e = check_cuda(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
-                               "cudaFuncSetAttribute(paged_token_kernel)");
-      if (e != BSA_OK) return e;
-    }
+    // At most 16.4 KB beside 17.2 KB of static shared memory: no opt-in (which is the function's, not
+    // the call's: one of this call's size would lower the limit under a call of another thread).
+    constexpr int kStatic = kTokWarps * 16 * (D + 6) * 4 + 4 * kTokWarps;
+    static_assert((kPagedMaxR + 1) * 4 + kStatic <= 48 * 1024, "shared memory of the token kernel");
     kern<<<p.workers, kTokThreads, smem, st>>>(t);
     count_launch();
     int e = check_cuda(cudaGetLastError(), "paged_token_kernel");

@@ -1,6 +1,9 @@
 """GPU parity of the paged-cache and head-norm calls at their edges, vs the oracle (tolerances
 as derived in test_parity_paged.py)."""
 
+import ctypes
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -69,3 +72,52 @@ def test_a_bound_of_no_new_tokens():
     out = torch.full_like(q, 7.0)
     bsa.paged_chunk_attention(*args, _i32([0, 0, 0]), _i32([40, 6]), max_new=0, out=out)
     assert bsa.device_status()[0] == 0 and (out == 7.0).all()
+
+
+def test_threads_with_thousands_of_requests():
+    """Host threads whose calls have different numbers of requests (and so of shared memory) at
+    the same time, each on a stream of its own and straight into the C entry point, so that no
+    lock of the interpreter orders them: every call is accepted and right."""
+    bsa = _bsa()
+    from block_sparse_attention_tcgen05_b200 import _lib
+    lib = _lib.load()
+    g = torch.Generator().manual_seed(62)
+    kc = torch.randn(40, 1, 16, 64, generator=g).to(torch.bfloat16).to(DEV)
+    cache = _lib.PagedCache(kc.data_ptr(), kc.data_ptr(), 40, 16, 1, 64, _lib.BSA_BF16, 1024, 1024, 64, 1024, 1024, 64)
+
+    def case(R):
+        rng = np.random.default_rng(R)
+        q = torch.randn(1, R, 64, generator=g).to(torch.bfloat16).to(DEV)
+        return q, _i32(rng.integers(0, 40, (R, 5))), _i32(np.arange(R + 1)), _i32(rng.integers(0, 79, R))
+    cases = [case(R) for R in (4096, 2100, 4000, 2300)]
+    want = [bsa.paged_chunk_attention(c[0], kc, kc, *c[1:], max_new=1) for c in cases]
+    outs = [torch.zeros_like(w) for w in want]
+    spaces = [torch.empty(bsa.paged_attention_workspace_bytes(c[0], kc, c[1], 1), dtype=torch.uint8, device=DEV)
+              for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    refused = []
+
+    def work(i):
+        q, table, cu, ctx = cases[i]
+        R = q.shape[1]
+        heads, to = (_lib.Heads(t.data_ptr(), 0, R * 64, 64) for t in (q, outs[i]))
+        vp = ctypes.c_void_p
+        args = (heads, cache, vp(table.data_ptr()), 5, 5, vp(cu.data_ptr()), vp(ctx.data_ptr()), R, R, 1, 1, vp(0), 0,
+                0, 0.0, 1, to, vp(spaces[i].data_ptr()), spaces[i].numel(), vp(streams[i].cuda_stream))
+        for _ in range(2000):
+            st = lib.bsa_paged_chunk_attention(*args)
+            if st:
+                refused.append((R, st))
+                return
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not refused, refused
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    q, table, cu, ctx = cases[1]
+    _check(want[1], q, kc, kc, table.cpu().numpy(), cu.cpu().numpy(), ctx.cpu().numpy(), True, None)
+    assert bsa.device_status()[0] == 0
