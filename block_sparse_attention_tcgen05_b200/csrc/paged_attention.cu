@@ -731,6 +731,64 @@ __device__ __forceinline__ float* tile_part_ml(const PagedArgs& a, int D) {
   return a.part + static_cast<size_t>(kTileSlots) * kTileRows * D;
 }
 
+// A softmax warp's chunks in an exact pass of the tile kernel: as its loop, 32 keys at a time, with
+// the reference and the largest logit taken before the scale. A function of its own, so that the
+// loop keeps its registers (inlined it cost that loop 1.6 %).
+struct ExactPass {
+  uint32_t bar0, tS;
+  const TileInfo* info;
+  volatile int* abort_flag;
+  int t, hb, lim, lim_tile;
+  float base, scale_log2;
+};
+template <typename T>
+__device__ __noinline__ bool exact_pass(const ExactPass& e, float* largest, float* sum, int* chunks) {
+  auto wait_all = [&](int bar, uint32_t parity, int site) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait_poll(e.bar0 + 8u * bar, parity, e.abort_flag, site));
+  };
+  float seen = -INFINITY, l = 0.f;
+  int nch = 0;
+#pragma unroll 1
+  for (int j = 0;; ++j) {
+    if (!wait_all(TB_INFO + j % kTileInfo, (j / kTileInfo) & 1, kPagedSite + 30)) return false;
+    const TileInfo* ti = e.info + j % kTileInfo;
+    if (ti->rows == 0) break;
+    const bool edge = ti->last > e.lim_tile, has = ti->rows > 64 * e.hb;
+    ++nch;
+    if (!has) break;  // (the last chunk)
+    if (!wait_all(TB_S + 2 * e.t + e.hb, j & 1, kPagedSite + 31)) return false;
+    tc_fence_after();
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      float v[32];
+      tmem_ld32(e.tS + 32 * i, v);
+      tmem_wait_ld();
+      uint32_t w[16];
+      const int vis0 = edge ? e.lim - ti->pos[4 * e.hb + 2 * i] : 16;  // last visible column of a granule
+      const int vis1 = edge ? e.lim - ti->pos[4 * e.hb + 2 * i + 1] : 16;
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        if (c % 16 > (c < 16 ? vis0 : vis1)) v[c] = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        seen = max3(seen, v[2 * c], v[2 * c + 1]);
+        const float x0 = ex2((v[2 * c] - e.base) * e.scale_log2), x1 = ex2((v[2 * c + 1] - e.base) * e.scale_log2);
+        l += x0 + x1;
+        w[c] = pack_pair<T>(x0, x1);
+      }
+      tmem_st16(e.tS + 16 * i, w);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(e.bar0 + 8u * (TB_P + 2 * e.t + e.hb));
+  }
+  *largest = seen;
+  *sum = l;
+  *chunks = nch;
+  return true;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kTileThreads, 1)
     paged_tile_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -747,7 +805,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ids + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* never = reinterpret_cast<int*>(tmem_slot + 2);
-  volatile int* redo = reinterpret_cast<volatile int*>(tmem_slot + 3);
+  int* more = reinterpret_cast<int*>(tmem_slot + 3);  // passes behind the first
   TileJob* where = reinterpret_cast<TileJob*>(tmem_slot + 4);  // r < 0: none
   static_assert(8 * TB_COUNT + kTileInfo * sizeof(TileInfo) + 8 * 4 + 4 * 4 + sizeof(TileJob) <= 512, "MISC");
   volatile float* s_max = reinterpret_cast<volatile float*>(misc + 512);  // (tile, half, row)
@@ -781,7 +839,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (lane == 0) {
       *abort_flag = 0;
       *never = 0;
-      *redo = 0;
+      *more = 0;
       prefetch_tmap(&tmK);
       prefetch_tmap(&tmV);
     }
@@ -824,8 +882,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   // is safe while no later logit is more than kExcess above it (base-2 units; the weights stay in
   // the type's range, and sums and outputs far inside fp32's). Each thread keeps the largest
   // logit that it saw; if some row went past the limit, the whole CTA does its work once
-  // more, relative to the rows' largest logits of all, which cannot fail.
+  // more, relative to the rows' largest logits of all, which cannot fail below kExact. A logit or
+  // reference of that size and more, of either sign, is rounded by half a unit and more when it is
+  // scaled (past 2^28 by as much as the weights' range), and what lies that far from the reference
+  // keeps nothing of a logit below it. Such a CTA does two more passes, one for the rows' largest
+  // logits before the scale, one that subtracts them before it scales.
   constexpr float kExcess = kF16 ? 14.f : 60.f;
+  constexpr float kExact = 4194304.f;
   const int t = (warp >> 3) & 1, hb = (warp >> 2) & 1, rr = tid & 127;
   const int row = row0 + 128 * t + rr;
   const bool live = warp < 16 && 128 * t + rr < rows;
@@ -842,12 +905,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   float m_row = -INFINITY, l_run = 0.f;
   int nch = 0;
   bool ok_all = true;
-  // The end of a pass, for every thread of the CTA: true when it was the last one.
+  // The end of a pass, for every thread of the CTA: true when it was the last one (the first pass
+  // says how many more there are).
   auto last_pass = [&](int pass) -> bool {
     tc_fence_before();
     named_bar_sync(1, kTileThreads);
     tc_fence_after();
-    return pass == 1 || *redo == 0;
+    return pass == *reinterpret_cast<volatile int*>(more);
   };
   if (warp >= 16) {
     // registers go from the last warpgroup to the softmax warpgroups
@@ -1121,10 +1185,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int lim_tile = a.causal ? min(q.len - 1, q.ctx + (row0 + 128 * t) / a.G) : q.len - 1;
       float seen = -INFINITY;  // largest logit (times the scale, base 2)
       bool ok = t == 0 || two;
+      const bool exact = pass > 0 && *reinterpret_cast<volatile int*>(more) == 2;
       l_run = 0.f;
       nch = 0;
 #pragma unroll 1
-      for (int j = 0; ok; ++j) {
+      for (int j = 0; ok && !exact; ++j) {
         if (!(ok = wait_all(TBAR(TB_INFO + j % kTileInfo), (j / kTileInfo) & 1, kPagedSite + 30))) break;
         const TileInfo* ti = info + j % kTileInfo;
         if (ti->rows == 0) break;
@@ -1181,18 +1246,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         l_run += (s0 + s1) + (s2 + s3);
         seen = max3(seen, q0, q1);  // relative to the row's reference
       }
+      if (exact && ok) {
+        const ExactPass e{bar0, tS, info, abort_flag, t, hb, lim, lim_tile,
+                          pass == 1 || m_row == -INFINITY ? 0.f : m_row, a.scale_log2};
+        ok = exact_pass<T>(e, &seen, &l_run, &nch);
+        if (pass == 2) m_row *= a.scale_log2;
+      }
       ok_all = ok || !(t == 0 || two);
-      // A row that the reference is too low for: its largest logit of all goes to both halves.
-      // So it does where the first chunk gave no reference (all its logits -infinity).
-      const bool low = seen > kExcess || (m_row == -INFINITY && seen > -INFINITY);
-      if (__any_sync(0xffffffffu, live && low) && lane == 0) *redo = 1;
+      if (pass == 0 && live) {
+        // A row that the reference is too low for: its largest logit of all goes to both halves.
+        // So it does where the first chunk gave no reference (all its logits -infinity).
+        const bool low = seen > kExcess || (m_row == -INFINITY && seen > -INFINITY);
+        const float size = fabsf(m_row == -INFINITY ? seen : m_row);
+        const bool large = (size >= kExact && size < INFINITY) || seen >= kExact;
+        if (low || large) atomicMax(more, large ? 2 : 1);
+      }
       if (last_pass(pass)) break;
       // The words that held the halves' first maxima serve again only here: every thread of the CTA
       // has passed the barrier, so both halves have taken their references from them.
       *xmine = seen;
       named_bar_sync(2, 512);  // the softmax warps
       const float most = fmaxf(seen, *xother);
-      m_row = m_row > -INFINITY ? m_row + fmaxf(most, 0.f) : most;
+      if (exact) m_row = most;
+      else m_row = m_row > -INFINITY ? m_row + fmaxf(most, 0.f) : most;
       named_bar_sync(1, kTileThreads);
     }
     // (every product and copy has ended) the sums of a row's halves, through the first stage

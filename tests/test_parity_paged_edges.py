@@ -121,3 +121,63 @@ def test_threads_with_thousands_of_requests():
     q, table, cu, ctx = cases[1]
     _check(want[1], q, kc, kc, table.cpu().numpy(), cu.cpu().numpy(), ctx.cpu().numpy(), True, None)
     assert bsa.device_status()[0] == 0
+
+
+@pytest.mark.parametrize("ctx,n", [(600, 40), (2300, 20), (100, 60), (600, 1)])
+@pytest.mark.parametrize("dt,D", [(torch.bfloat16, 128), (torch.float16, 64)])
+def test_first_keys_far_below(ctx, n, dt, D):
+    """The first 128 keys' logits are finite and so far below the later ones (2^29 base-2 units in
+    fp16, 2^99 in bf16) that a difference from them keeps nothing of a later logit; those reach
+    from some 30 to above 100 units."""
+    bsa = _bsa()
+    q, kc, vc, table, cu, _ = _attention_case(63, [ctx], [n], 2, 1, D, 64, dt)
+    used = table[0]
+    far = 65504.0 if dt == torch.float16 else 1e15
+    q[0] *= 8.0
+    q[1] *= 30.0
+    q[..., 0] = far
+    kc[..., 0] = 0.0
+    kc[used[:2], :, :, 0] = -far
+    rest = kc[used[-1], :, (ctx + n) % 64:] if (ctx + n) % 64 else kc[used[-1], :, :0]
+    rest.fill_(float("nan"))
+    out = bsa.paged_chunk_attention(q, kc, vc, _i32(table), _i32(cu), _i32([ctx]), causal=True, max_new=n)
+    assert bsa.device_status() == (0, 0)
+    if ctx < 128:  # rows that see only such keys have a softmax of differences past 2^20: a mean
+        seen = vc[used[:2], 0].reshape(-1, D)[:ctx + 1].float()
+        assert torch.isfinite(out[:, :n]).all()
+        assert (out[:, 0] <= seen.amax(0)).all() and (out[:, 0] >= seen.amin(0)).all()
+        return
+    mask = np.ones((1, 1, len(used)), dtype=bool)
+    mask[..., :2] = False
+    clean, qc = kc.clone(), q.clone()
+    clean[used[:2]] = 0.0
+    qc[..., 0] = 0.0
+    _check(out, qc, clean, vc, table, cu, [ctx], True, mask)
+
+
+@pytest.mark.parametrize("ctx,n", [(600, 40), (2300, 20), (90, 30), (600, 1)])
+@pytest.mark.parametrize("dt,D,sign", [(torch.bfloat16, 128, 1), (torch.bfloat16, 64, -1), (torch.float16, 64, 1),
+                                       (torch.float16, 128, -1)])
+def test_logits_past_the_weights_range(ctx, n, dt, D, sign):
+    """All logits of a row have one size, up to 2^30 base-2 units in fp16 and 2^60 in bf16, where one
+    rounding of a logit is more than the weights' range: equal logits give the mean of the
+    values, a few larger ones theirs."""
+    bsa = _bsa()
+    q, kc, vc, table, cu, _ = _attention_case(64, [ctx], [n], 3, 1, D, 64, dt)
+    live = ~torch.isnan(kc[..., :1])
+    top = 65504.0 if dt == torch.float16 else 2.0 ** 30
+    q.zero_()
+    q[..., 0] = sign * top * (0.5 + 0.5 * torch.rand(q.shape[:2], generator=torch.Generator().manual_seed(65))).to(DEV)
+    kc.copy_(torch.where(live, torch.zeros_like(kc), kc))
+    kc[..., 0] = torch.where(live[..., 0], torch.full_like(kc[..., 0], top / 2), kc[..., 0])
+    args = (kc, vc, _i32(table), _i32(cu), _i32([ctx]))
+    out = bsa.paged_chunk_attention(q, *args, causal=True, max_new=n)
+    assert bsa.device_status() == (0, 0)
+    _check(out, torch.zeros_like(q), torch.zeros_like(kc), vc, table, cu, [ctx], True, None)
+    # one key of twice the size, or half of it where the sign asks for that
+    used = table[0]
+    kc[used[1], :, 5, 0] = top if sign > 0 else top / 4
+    out = bsa.paged_chunk_attention(q, *args, causal=True, max_new=n)
+    want = vc[used[1], 0, 5]
+    if ctx >= 70:
+        assert torch.equal(out[:, :n], want.expand(3, n, D))
