@@ -137,11 +137,17 @@ _native = None
 
 def native():
     """The native marshalling module (built in-tree by ``build.py`` beside libbsa.so). Raises
-    if it is missing."""
+    if it is missing, or was built against another torch or interpreter."""
     global _native
     if _native is None:
         import importlib
+        from . import build
         load()
+        if os.path.exists(build.NATIVE):
+            with open(build.NATIVE, "rb") as f:
+                if build.native_id().encode() not in f.read():
+                    raise RuntimeError("_native.so was built against another torch or Python; build it with "
+                                       "`python -m block_sparse_attention_tcgen05_b200.build`")
         try:
             _native = importlib.import_module("block_sparse_attention_tcgen05_b200._native")
         except ImportError as e:

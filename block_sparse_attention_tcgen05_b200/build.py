@@ -37,6 +37,25 @@ def up_to_date():
     return all(os.path.getmtime(s) <= t for s in sources())
 
 
+def native_id():
+    """What _native.so is compiled against, as it holds it: torch's C++ ABI changes with its version,
+    the interpreter's with its own."""
+    import torch
+    return f"bsa native module for torch {torch.__version__}, {sys.implementation.cache_tag};"
+
+
+def native_up_to_date():
+    """Whether _native.so is newer than its sources and was built against this torch and
+    interpreter."""
+    if not os.path.exists(NATIVE):
+        return False
+    t = os.path.getmtime(NATIVE)
+    if any(os.path.getmtime(s) > t for s in (NATIVE_SRC, os.path.join(ROOT, "include", "bsa.h"))):
+        return False
+    with open(NATIVE, "rb") as f:
+        return native_id().encode() in f.read()
+
+
 def _native_command(out):
     import torch
     t = os.path.dirname(torch.__file__)
@@ -44,6 +63,7 @@ def _native_command(out):
            sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f'-DBSA_NATIVE_ID="{native_id()}"',
             *[x for i in inc for x in ("-isystem", i)], NATIVE_SRC, "-o", out,
             "-L", HERE, "-l:libbsa.so", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(t, "lib"),
             "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
@@ -62,16 +82,15 @@ def _compile(cmd, out, verbose):
 
 
 def build_native(force=False, verbose=False):
-    """Compile _native.so unless it is newer than its sources. Returns its path."""
-    srcs = (NATIVE_SRC, os.path.join(ROOT, "include", "bsa.h"))
-    if force or not os.path.exists(NATIVE) or any(os.path.getmtime(s) > os.path.getmtime(NATIVE) for s in srcs):
+    """Compile _native.so unless it is up to date. Returns its path."""
+    if force or not native_up_to_date():
         _compile(_native_command(NATIVE + ".tmp"), NATIVE, verbose)
     return NATIVE
 
 
 def build(force=False, verbose=False, extra=()):
-    """Compile libbsa.so and _native.so unless they are newer than their sources. Returns the
-    path of libbsa.so."""
+    """Compile libbsa.so and _native.so unless they are up to date. Returns the path of
+    libbsa.so."""
     if force or not up_to_date():
         _compile([NVCC, *FLAGS, *extra, SRC, "-o", LIB + ".tmp"], LIB, verbose)
     build_native(force, verbose)

@@ -577,6 +577,9 @@ PyMethodDef kMethods[] = {
     BSA_METHOD("paged_chunk_attention", attend, 12),
     {nullptr, nullptr, 0, nullptr}};
 
+// What the module was compiled against; build.py and the loader look for it in the file.
+[[gnu::used]] const char kNativeId[] = BSA_NATIVE_ID;
+
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_native", "Native marshalling of libbsa calls.", -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};
 
