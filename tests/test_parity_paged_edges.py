@@ -181,3 +181,47 @@ def test_logits_past_the_weights_range(ctx, n, dt, D, sign):
     want = vc[used[1], 0, 5]
     if ctx >= 70:
         assert torch.equal(out[:, :n], want.expand(3, n, D))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("ctx,new", [([90, 5, 200, 31], [1, 2, 1, 1]), ([90, 5, 1900, 31, 3], [20, 30, 90, 17, 60]),
+                                     ([300, 0, 40], [40, 1, 9])])
+def test_heads_without_a_page_get_exact_zeros(causal, ctx, new):
+    """Every (request, KV head) whose mask keeps none of its pages, among others that keep some:
+    rows of zeros, whatever stood there, in both kernels."""
+    bsa = _bsa()
+    q, kc, vc, table, cu, mask = _attention_case(66, ctx, new, 6, 3, 64, 16, torch.float16, 0.5)
+    rng = np.random.default_rng(67)
+    need = [-(-(c + n) // 16) for c, n in zip(ctx, new)]
+    empty = rng.random((len(ctx), 3)) < 0.4
+    empty[0] = [False, True, False]
+    for r, h in np.argwhere(empty):
+        mask[r, h, :need[r]] = False
+        for j in range(need[r]):
+            kc[table[r, j], h] = float("nan")
+            vc[table[r, j], h] = float("nan")
+    out = torch.full_like(q, 7.0)
+    bsa.paged_chunk_attention(q, kc, vc, _i32(table), _i32(cu), _i32(ctx), causal=causal, max_new=max(new),
+                              page_mask=torch.from_numpy(mask).to(DEV), out=out)
+    assert bsa.device_status() == (0, 0) and (out[:, cu[-1]:] == 7.0).all()
+    none = [(r, h) for r in range(len(ctx)) for h in range(3) if not mask[r, h, :need[r]].any()]
+    assert len(none) >= empty.sum() > 0 and len(none) < 3 * len(ctx)
+    for r, h in none:
+        assert (out[2 * h:2 * h + 2, cu[r]:cu[r + 1]] == 0).all()
+    _check(out, q, kc, vc, table, cu, ctx, causal, mask)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_a_cache_laid_out_token_by_token(n):
+    """Pages whose rows hold all heads of a token (a row's stride above a head's), of a wider
+    buffer: the same bits as of the cache laid out by heads."""
+    bsa = _bsa()
+    q, kc, vc, table, cu, _ = _attention_case(68, [300, 77], [n, n], 6, 3, 64, 32, torch.bfloat16)
+    wide = torch.full((kc.shape[0], 32, 2, 4, 64), float("nan"), dtype=kc.dtype, device=DEV)
+    wide[:, :, 0, :3], wide[:, :, 1, :3] = kc.transpose(1, 2), vc.transpose(1, 2)
+    k2, v2 = (wide[:, :, i, :3].transpose(1, 2) for i in range(2))
+    args = (_i32(table), _i32(cu), _i32([300, 77]))
+    want = bsa.paged_chunk_attention(q, kc, vc, *args, max_new=n)
+    got = bsa.paged_chunk_attention(q, k2, v2, *args, max_new=n)
+    assert bsa.device_status() == (0, 0) and torch.equal(got[:, :2 * n], want[:, :2 * n])
+    _check(got, q, kc, vc, table, cu, [300, 77], True, None)
