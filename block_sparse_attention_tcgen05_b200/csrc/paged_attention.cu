@@ -9,13 +9,15 @@
 //       way. The (request, head, 64-key chunk) space is cut into equal contiguous spans, one
 //       per CTA, so ragged lengths balance; a (request, head) that crosses a span border
 //       leaves partial results that token_combine_kernel joins. 64 requests of 11000 keys on
-//       average (24 / 8 heads of 128): 447 us, the cache's bytes at the measured copy rate; one
-//       request of 32761 keys: 31 us, floor 20 us, the rest is the way from the lengths over the
-//       pages to the first keys, and the join.
+//       average (24 / 8 heads of 128): 448 us, the cache's bytes at the measured copy rate; one
+//       request of 32761 keys: 32 us, floor 20 us, the rest is the way from the lengths over the
+//       pages to the first keys, and the join. Spans are cut by the requests' lengths alone, so
+//       masked pages count as work: the 64 requests with two pages of five kept at random take 230
+//       us in single calls, floor 179.
 //   paged_tile_kernel   more rows. tcgen05: two 128-row tiles per CTA over 128-key chunks
 //       gathered page by page with TMA, logits and weights in TMEM, two softmax threads per
 //       row. Long requests are split over CTAs and tile_combine_kernel joins the parts. 1560
-//       rows of 40 heads over 32760 keys: 978 us in single calls (1070 TFLOP/s, 0.65 of the
+//       rows of 40 heads over 32760 keys: 970 us in single calls (1080 TFLOP/s, 0.65 of the
 //       burst peak), 1.13 ms in calls without a pause, where the power limit lowers the
 //       clocks. Of a chunk's 3400 cycles the tensor core works 2600 and the exponentials take
 //       2050 of the special-function units; the rest is what passes between the two.
@@ -613,10 +615,13 @@ enum {
 // keys are split over CTAs so that none has many more than `quantum` chunks of 128 keys. With
 // `share` the chunks of one SM if the whole call's were spread evenly: half the share where it is
 // long (32 chunks, some 60 us), so that long requests are split among short ones and the last
-// CTA ends little after the others; the share itself where it is short, so that one wave does
-// it all; and at least kTileMinChunks, since a CTA costs about as much as 4 chunks to start and
-// end. With many more pairs than SMs none is split. All of it follows from the lengths,
-// which live on the GPU, so each CTA works it out.
+// CTA ends little after the others; the share itself where it is short; and at least
+// kTileMinChunks, since a CTA costs about as much as 4 chunks to start and end. A quantum below
+// kTileLongShare, which a share of up to 63 chunks gives, then grows in calls of up to 32 requests
+// until one wave does it all or nothing is split any more. With many more pairs than SMs none is
+// split. Chunks are counted by the requests' lengths alone: a page mask, and the keys that a causal
+// tile does not see, are not taken off. All of it follows from the lengths, which live on the GPU, so
+// each CTA works it out.
 constexpr int kTileSms = 148;
 constexpr int kTileJobs = 2 * kTileSms;  // the quantum is never below the work over this
 constexpr int kTileLongShare = 32;
@@ -674,7 +679,8 @@ __device__ __forceinline__ bool find_tile(const PagedArgs& a, int u, int lane, T
     quantum = tile_quantum(a, work);
     // Rounding up makes more jobs than the share allows for; where one wave is to do it all, the
     // quantum grows until it does (40 pairs of 68 chunks: 120 jobs of 23 chunks, 64 us; as 160 jobs
-    // of 17 chunks, in two waves, 75).
+    // of 17 chunks, in two waves, 75), or until nothing is left to split (43 pairs of 2 to 68 chunks,
+    // share 36: 372 jobs at a quantum of 18, 228 at 46, then 172 whole ones).
     if (a.R <= 32 && quantum < kTileLongShare) {
       for (int i = 0; i < 4; ++i) {
         const int jobs = __reduce_add_sync(0xffffffffu, pairs * tile_splits(chunks, quantum)) * a.Hkv;
@@ -881,12 +887,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   // for good: nothing of a chunk waits for its maximum, and the output is never rescaled. That
   // is safe while no later logit is more than kExcess above it (base-2 units; the weights stay in
   // the type's range, and sums and outputs far inside fp32's). Each thread keeps the largest
-  // logit that it saw; if some row went past the limit, the whole CTA does its work once
-  // more, relative to the rows' largest logits of all, which cannot fail below kExact. A logit or
-  // reference of that size and more, of either sign, is rounded by half a unit and more when it is
-  // scaled (past 2^28 by as much as the weights' range), and what lies that far from the reference
-  // keeps nothing of a logit below it. Such a CTA does two more passes, one for the rows' largest
-  // logits before the scale, one that subtracts them before it scales.
+  // logit that it saw; if some row went past the limit (fp16: 9.7 nats above its first 128 keys), the
+  // whole CTA does its work once more, relative to the rows' largest logits of all, which cannot fail
+  // below kExact (1560 rows of 40 heads over 15600 keys, fp16: 460 us, and 880 with such a row in
+  // every CTA). A logit or reference of that size and more, of either sign, is rounded by a quarter of
+  // a unit and more when it is scaled (past 2^28 by as much as the weights' range), and a difference
+  // that large keeps little or nothing of a smaller logit. Such a CTA does two more passes, one for the
+  // rows' largest logits before the scale, one that subtracts them before it scales.
   constexpr float kExcess = kF16 ? 14.f : 60.f;
   constexpr float kExact = 4194304.f;
   const int t = (warp >> 3) & 1, hb = (warp >> 2) & 1, rr = tid & 127;

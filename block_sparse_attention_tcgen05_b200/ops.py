@@ -579,8 +579,8 @@ def paged_chunk_attention(q, k_cache, v_cache, block_table, cu_new, context_lens
     0 counts as 1); a request with more, or with keys past its row of the table, is recorded in
     the device status.
     ``page_mask`` bool/uint8 (R, width) or (R, Hkv, width) keeps the pages that are not zero,
-    shared by a KV head's query heads; a row that no key is left for gets 0. bf16 or fp16,
-    D in {64, 128}. Returns q's type (Hq,T,D); rows from ``cu_new[R]`` on are not written."""
+    shared by a KV head's query heads; a row that no key is left for gets 0. ``scale``: default,
+    and for 0 or less, 1/sqrt(D). bf16 or fp16, D in {64, 128}. Returns q's type (Hq,T,D); rows from ``cu_new[R]`` on are not written."""
     return _lib.native().paged_chunk_attention(q, k_cache, v_cache, block_table, cu_new,
                                                context_lens, causal, max_new, page_mask, scale,
                                                out, workspace)

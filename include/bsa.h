@@ -623,7 +623,8 @@ int bsa_paged_qk_norm_append(bsa_heads q, bsa_heads k, bsa_heads v, int T, int H
  * tokens of the chunk that do not see it (their weight 0 times it). Hq a multiple of Hkv. fp32
  * logits, sums and accumulators; the weights, up to 2^60 before the sum divides them (bf16; fp16
  * 2^14), are rounded to the cache's type before the second product: values of magnitude up to
- * 2^39 cannot overflow. Limits: T * Hq <= 2^30, a
+ * 2^39 cannot overflow, and fp16 drops from the product, not from the sum, what weighs less than
+ * 2^-25 of the row's reference. Limits: T * Hq <= 2^30, a
  * block-table row of at most 2^28 keys, all of them together 2^36. A workspace belongs to one
  * call at a time, replays of a graph that captured it included.
  */
